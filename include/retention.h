@@ -75,7 +75,10 @@ typedef enum {
                                 ret_last_device_status)                        */
 } ret_status;
 
-typedef enum { RET_F32 = 0, RET_BF16 = 1 } ret_dtype;
+/* RET_I8 (signed, -127..127) and RET_E4M3 (8-bit floats, 4 exponent and 3
+ * mantissa bits, largest value 448) are codes with scales; only ret_rms_norm
+ * writes them and only ret_matvec_w4 reads them. */
+typedef enum { RET_F32 = 0, RET_BF16 = 1, RET_I8 = 2, RET_E4M3 = 3 } ret_dtype;
 
 /* Problem description.  The struct is read during the call only. */
 typedef struct {
@@ -515,6 +518,154 @@ ret_status ret_gate_norm_backward(int B, int L, int H, int d_v, int o_dtype,
                                   const void *O, int g_dtype, const void *G,
                                   const void *dY, float eps, void *dO, void *dG,
                                   void *stream);
+
+/* --------------------------------------------------------------------------
+ * Operators around the recurrent mixers when they serve: the block's norm, the
+ * products of a token with 4-bit weights, and the selective scan with its
+ * convolution.  No counterpart in the paper summary, whose layer they extend.
+ *
+ * Operands described as "strided rows" are rows of a wider matrix (columns of
+ * a projection's output, say): row r starts at base + r*ld elements, ld at
+ * least the row's length, and the base need only be aligned to its element.
+ * They are read in 16-byte pieces where base and ld are multiples of 16 bytes,
+ * element by element otherwise.  Every other pointer is 16-byte aligned, as
+ * above (`lengths`: 4 bytes).  Parameters (norm and convolution weights, A,
+ * biases) are fp32.  No output may overlap an input except where said.  All
+ * arithmetic is fp32; each output is rounded once.  These calls launch one
+ * kernel, use no workspace, and may run at once on any streams.
+ * -------------------------------------------------------------------------- */
+
+#define RET_MAX_NORM_WIDTH 16384 /* channels of a ret_rms_norm row           */
+#define RET_MAX_CONV_WIDTH 4     /* taps of ret_causal_conv                  */
+#define RET_MAX_SCAN_STATES 128  /* states per channel of ret_selective_scan */
+#define RET_MAX_MATVEC_ROWS 64   /* rows of one ret_matvec_w4                */
+
+/*
+ * ret_rms_norm -- the residual's addition and the root-mean-square norm of
+ * `rows` rows of d channels:
+ *     s = x + r,   r_out = s,   y = w s / sqrt(mean(s^2) + eps)
+ * (the norm is taken of s before r_out's rounding), with y in fp32 or bf16, or
+ * in 8 bits: per row and group of `group` channels (0: the whole row)
+ *     scale = max |y| / top,   code = round(y / scale)
+ * with top = 127 for RET_I8 and 448 for RET_E4M3, to nearest even.  A group
+ * whose scale would be below 2^-119 (all zeros, say) has scale 0 and codes 0;
+ * one with a y that is not finite has scale NaN (codes 0), so that every value
+ * it stands for is NaN.
+ *   X       device x_dtype (F32, BF16), strided rows of d
+ *   w       device fp32 [d], or NULL (ones)
+ *   R       device r_dtype (F32, BF16) [rows][d], or NULL (no residual)
+ *   R_out   device r_dtype [rows][d], or NULL; may be R.  Needs R.
+ *   Y       device y_dtype [rows][d], fully overwritten
+ *   scales  device fp32 [rows][d / group]; for 8-bit y only
+ * 1 <= d <= RET_MAX_NORM_WIDTH; group 0, or 32, 64 or 128 dividing d (0 for
+ * fp32 and bf16 y).  Errors: RET_ERR_NULL, _SHAPE, _DTYPE, _ALIGN, _ARG (eps),
+ * _UNSUPPORTED, _CUDA.
+ */
+ret_status ret_rms_norm(long long rows, int d, int x_dtype, const void *X,
+                        long long ldx, const float *w, int r_dtype,
+                        const void *R, void *R_out, float eps, int y_dtype,
+                        void *Y, int group, float *scales, void *stream);
+
+/*
+ * ret_causal_conv -- the short causal convolution along the rows of each of D
+ * channels, as it precedes ret_selective_scan:
+ *     y_t = f(bias + sum_{k < width} W[k] x_{t - width + 1 + k}),
+ * f the swish x sigmoid(x) or (swish = 0) the identity.  Rows before the first
+ * come from state_in, the width - 1 inputs before row 0, oldest first.
+ *   X       device dtype (F32, BF16), strided rows: row t of sequence b at
+ *           X + (b*L + t)*ldx
+ *   W       device fp32 [D][width];  bias device fp32 [D] or NULL
+ *   lengths device int32 [B] or NULL: sequence b has lengths[b] rows (taken
+ *           into 0..L); later rows of X are not read, later rows of Y are left
+ *           as they were, and the state is the one after row lengths[b] - 1
+ *   state_in, state_out  device dtype [B][width-1][D], or NULL (zeros; not
+ *           wanted); state_out may be state_in
+ *   Y       device dtype [B][L][D]
+ * Single tokens: L = 1 with state_out = state_in.  2 <= width <=
+ * RET_MAX_CONV_WIDTH.  Errors: RET_ERR_NULL, _SHAPE, _DTYPE, _ALIGN, _ARG
+ * (swish), _UNSUPPORTED, _CUDA.
+ */
+ret_status ret_causal_conv(int B, int L, int D, int width, int dtype,
+                           const void *X, long long ldx, const float *W,
+                           const float *bias, int swish, const int *lengths,
+                           const void *state_in, void *state_out, void *Y,
+                           void *stream);
+
+/* Problem description of ret_selective_scan; read during the call only. */
+typedef struct {
+    int B, L, D, N;        /* sequences, rows, channels, states per channel   */
+    int G;                 /* groups of D / G adjacent channels that share B, C */
+    int dtype;             /* ret_dtype of U, delta, Z, Bm, Cm and Y          */
+    int softplus;          /* 1: d = log(1 + exp(delta + bias)); 0: delta + bias */
+    long long ldu, ldd, ldz, ldb, ldc; /* leading dimensions, in elements     */
+} ret_scan_desc;
+
+/*
+ * ret_selective_scan -- the diagonal state space recurrence whose step size,
+ * input and output maps depend on the token: per channel c of group g, with
+ * N states,
+ *     d_t = softplus(delta_t + delta_bias)
+ *     h_t[n] = exp(d_t A[c][n]) h_{t-1}[n] + d_t u_t B_t[g][n]
+ *     y_t = (sum_n C_t[g][n] h_t[n] + skip u_t) swish(z_t)
+ * (update first, then read, as ret_recurrent_step).  The sibling of
+ * ret_chunkwise with a decay per token, channel and state.  A is meant to be
+ * negative.
+ *   U, delta, Z  device dtype, strided rows of D (row t of sequence b is row
+ *           b*L + t); Z NULL: no gate
+ *   Bm, Cm  device dtype, strided rows of G*N
+ *   A       device fp32 [D][N];  delta_bias, skip  device fp32 [D] or NULL
+ *   lengths device int32 [B] or NULL, as for ret_causal_conv
+ *   state_in, state_out  device fp32 [B][D][N], or NULL (zeros; not wanted);
+ *           state_out may be state_in
+ *   Y       device dtype [B][L][D]
+ * Single tokens: L = 1 with state_out = state_in.  1 <= N <=
+ * RET_MAX_SCAN_STATES, G divides D.  Errors: RET_ERR_NULL, _SHAPE, _DTYPE,
+ * _ALIGN, _ARG (softplus), _UNSUPPORTED, _CUDA.
+ */
+ret_status ret_selective_scan(const ret_scan_desc *desc, const void *U,
+                              const void *delta, const float *delta_bias,
+                              const float *A, const void *Bm, const void *Cm,
+                              const float *skip, const void *Z,
+                              const int *lengths, const float *state_in,
+                              float *state_out, void *Y, void *stream);
+
+/*
+ * ret_matvec_w4 -- the product of a few rows with 4-bit weights, the
+ * projections of single tokens:
+ *     y[m][n] = sum_k w[n][k] x[m][k],
+ *     w[n][k] = scales[n][k / group] (q[n][k] - zeros[n][k / group]).
+ *   X       device x_dtype, strided rows: M rows of K values.  F32, BF16, or
+ *           8-bit codes that stand for code * x_scales
+ *   x_scales  device fp32 [M][K / x_group] (8-bit X only); x_group 0 means one
+ *           scale per row, otherwise a multiple of `group` that divides K
+ *   Wq      device, 4-bit codes [N][K/2] bytes: the low half of byte i of a
+ *           row is column 2i, the high half column 2i + 1
+ *   scales  device bf16 [N][K / group]
+ *   zeros   device uint8 [N][K / group], 0..15, or NULL (8 everywhere)
+ *   Y       device y_dtype (F32, BF16) [M][N]
+ * 0 <= M <= RET_MAX_MATVEC_ROWS, group 32, 64 or 128, K a multiple of it.  The
+ * products are exact and summed in fp32.  Errors: RET_ERR_NULL, _SHAPE,
+ * _DTYPE, _ALIGN, _UNSUPPORTED, _CUDA.
+ */
+ret_status ret_matvec_w4(int M, int N, int K, int group, int x_dtype,
+                         const void *X, long long ldx, const float *x_scales,
+                         int x_group, const void *Wq, const void *scales,
+                         const void *zeros, int y_dtype, void *Y, void *stream);
+
+/*
+ * ret_quantize_w4 -- codes, scales and zero points of ret_matvec_w4 from a
+ * weight matrix as ret_gemm_bf16 takes it (K rows of N).  Without zeros,
+ * scale = max |w| / 7 and code = 8 + round(w / scale); with them, scale =
+ * (max - min) / 15 over the group and 0, zero = round(-min / scale).  The codes
+ * are taken with the scale as rounded to bf16.
+ *   W       device w_dtype (F32, BF16), strided rows: K rows of N values
+ *   Wq, scales, zeros  device, as ret_matvec_w4 reads them, overwritten; zeros
+ *           may be NULL
+ * Errors: RET_ERR_NULL, _SHAPE, _DTYPE, _ALIGN, _UNSUPPORTED, _CUDA.
+ */
+ret_status ret_quantize_w4(int K, int N, int group, int w_dtype, const void *W,
+                           long long ldw, void *Wq, void *scales, void *zeros,
+                           void *stream);
 
 /* Synchronises `stream`, then returns and clears the device status word
  * that bounded waits in the kernels latch (RET_ERR_TIMEOUT), or

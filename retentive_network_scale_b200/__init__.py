@@ -9,7 +9,8 @@ from importlib import import_module
 
 _BINDING_NAMES = (
     "ret_parallel", "ret_chunkwise", "ret_chunkwise_gate_static", "ret_recurrent_step",
-    "ret_gate_norm",
+    "ret_gate_norm", "ret_rms_norm", "ret_causal_conv", "ret_selective_scan", "ret_matvec_w4",
+    "ret_quantize_w4",
     "ret_workspace_size", "ret_last_device_status", "ret_kernel_launches",
     "ret_status_string",
     "RetentionError", "msr_gammas", "load_library",

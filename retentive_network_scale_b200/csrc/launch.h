@@ -206,6 +206,8 @@ cudaError_t launch_parallel_tc(const Params &p, bool out_bf16, const void *Q, co
                                const void *V, void *O, void *workspace, int *status,
                                cudaStream_t st);
 
+// RET_OK when the current device is sm_100, RET_ERR_UNSUPPORTED otherwise.
+ret_status validate_device();
 // The description checks every entry point runs first (no CUDA calls).
 ret_status validate_desc(const ret_desc *d);
 // The kernels' parameters for a checked description.

@@ -20,7 +20,7 @@ import torch
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libretention.so")
 
-RET_F32, RET_BF16 = 0, 1
+RET_F32, RET_BF16, RET_I8, RET_E4M3 = 0, 1, 2, 3
 RET_MAX_HEADS = 128
 STATUS_NAMES = ["RET_OK", "RET_ERR_NULL", "RET_ERR_SHAPE", "RET_ERR_DTYPE", "RET_ERR_ALIGN",
                 "RET_ERR_ARG", "RET_ERR_WORKSPACE", "RET_ERR_UNSUPPORTED", "RET_ERR_CUDA",
@@ -37,10 +37,16 @@ EXPORTS = ("ret_parallel", "ret_parallel_workspace_size", "ret_chunkwise",
            "ret_segment_state", "ret_segment_state_workspace_size", "ret_state_scan",
            "ret_chunkwise_segmented", "ret_chunkwise_segmented_workspace_size",
            "ret_recurrent_step", "ret_gate_norm", "ret_gate_norm_backward", "ret_last_device_status",
-           "ret_kernel_launches", "ret_status_string", "ret_msr_gammas")
+           "ret_kernel_launches", "ret_status_string", "ret_msr_gammas",
+           "ret_rms_norm", "ret_causal_conv", "ret_selective_scan", "ret_matvec_w4",
+           "ret_quantize_w4")
 RET_STATIC_SCRATCH_FLOATS = 4 << 20
 RET_MAX_DECODE_STEPS = 16
 RET_MAX_SEGMENTS = 64
+RET_MAX_NORM_WIDTH = 16384
+RET_MAX_CONV_WIDTH = 4
+RET_MAX_SCAN_STATES = 128
+RET_MAX_MATVEC_ROWS = 64
 
 
 class RetentionError(RuntimeError):
@@ -59,6 +65,11 @@ class RetDesc(ctypes.Structure):
         ("rotate", ctypes.c_int), ("theta_base", ctypes.c_double),
         ("pos_offset", ctypes.c_longlong),
     ]
+
+
+class RetScanDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("B", "L", "D", "N", "G", "dtype", "softplus")] + \
+               [(n, ctypes.c_longlong) for n in ("ldu", "ldd", "ldz", "ldb", "ldc")]
 
 
 _lib = None
@@ -120,6 +131,12 @@ def load_library(path: str = LIB_PATH):
                                                        ctypes.c_int, vp, vp]
     lib.ret_gate_norm_backward.argtypes = [ctypes.c_int] * 5 + [vp, ctypes.c_int, vp, vp,
                                                                 ctypes.c_float, vp, vp, vp]
+    i, f = ctypes.c_int, ctypes.c_float
+    lib.ret_rms_norm.argtypes = [ll, i, i, vp, ll, vp, i, vp, vp, f, i, vp, i, vp, vp]
+    lib.ret_causal_conv.argtypes = [i, i, i, i, i, vp, ll, vp, vp, i, vp, vp, vp, vp, vp]
+    lib.ret_selective_scan.argtypes = [ctypes.POINTER(RetScanDesc)] + [vp] * 13
+    lib.ret_matvec_w4.argtypes = [i, i, i, i, i, vp, ll, vp, i, vp, vp, vp, i, vp, vp]
+    lib.ret_quantize_w4.argtypes = [i, i, i, i, vp, ll, vp, vp, vp, vp]
     lib.ret_last_device_status.argtypes = [vp]
     lib.ret_msr_gammas.argtypes = [ctypes.c_int, ctypes.POINTER(ctypes.c_double)]
     lib.ret_msr_gammas.restype = ctypes.c_int
@@ -634,6 +651,216 @@ def ret_gate_norm_backward(O, G, dY, dO, dG, eps=1e-5, stream=None):
                                       _ptr(G), _ptr(dY), float(eps), _ptr(dO), _ptr(dG),
                                       _stream(stream)), "ret_gate_norm_backward")
     return dO, dG
+
+
+# ------------------------------------------------- operators around the mixers
+_CODES = {torch.float32: RET_F32, torch.bfloat16: RET_BF16, torch.int8: RET_I8,
+          torch.float8_e4m3fn: RET_E4M3}
+
+
+def _on(t, name, shape, dtype, device):
+    """Address of a dense tensor of the call's device (None: 0)."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.get_device() != device:
+        raise TypeError(f"{name} must be a CUDA tensor on device {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _rows(t, name, shape, dtype, device):
+    """Address and leading dimension of strided rows: unit stride along the
+    last dimension, one stride between all rows before it."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.get_device() != device:
+        raise TypeError(f"{name} must be a CUDA tensor on device {device}")
+    n, stride = shape[-1], t.stride()
+    if n > 1 and stride[-1] != 1:
+        raise ValueError(f"{name} needs unit stride along its rows")
+    if len(shape) == 2:
+        ld = stride[0] if shape[0] > 1 else n
+    elif shape[1] > 1:
+        ld = stride[1]
+        if shape[0] > 1 and stride[0] != shape[1] * ld:
+            raise ValueError(f"{name} needs one stride between all its rows")
+    else:
+        ld = stride[0] if shape[0] > 1 else n
+    if ld < n:
+        raise ValueError(f"{name} has overlapping rows")
+    return t.data_ptr(), ld
+
+
+def _device_of(t, name):
+    """Device of a call: the tensor's, which must be the current one."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    device = t.get_device()
+    if device != torch.cuda.current_device():
+        raise ValueError(f"{name} is on device {device}, which is not the current one")
+    return device
+
+
+def _on_stream(stream, device):
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def ret_rms_norm(X, Y, weight=None, residual=None, residual_out=None, scales=None, eps=1e-5,
+                 stream=None):
+    """Y = weight s / sqrt(mean(s^2) + eps), s = X + residual (written to
+    residual_out, which may be residual), for rows [.., d] of X; the leading
+    dimensions of the other tensors are X's.  An int8 or float8_e4m3fn Y takes
+    scales [.., groups] (fp32): one per row, or per 32, 64 or 128 channels.
+    Returns Y."""
+    device = _device_of(X, "X")
+    shape = X.shape
+    d = shape[-1]
+    px, ldx = _rows(X, "X", shape, X.dtype, device)
+    rows = X.numel() // d if d else 0
+    y_dtype = _CODES.get(Y.dtype)
+    if y_dtype is None or X.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"unsupported dtypes {X.dtype} -> {Y.dtype}")
+    group, r_dtype = 0, RET_F32
+    if y_dtype >= RET_I8:
+        if scales is None:
+            raise ValueError("an 8-bit Y needs scales")
+        groups = scales.shape[-1]
+        if groups < 1 or d % groups:
+            raise ValueError("scales must divide the channels into equal groups")
+        group = 0 if groups == 1 else d // groups
+        ps = _on(scales, "scales", shape[:-1] + (groups,), torch.float32, device)
+    elif scales is not None:
+        raise ValueError("scales go with an 8-bit Y")
+    else:
+        ps = None
+    if residual is not None:
+        r_dtype = _dtype_code(residual)
+        if residual_out is not None and residual_out.dtype != residual.dtype:
+            raise TypeError("residual_out takes residual's dtype")
+    elif residual_out is not None:
+        raise ValueError("residual_out needs residual")
+    _check(load_library().ret_rms_norm(
+        rows, d, _dtype_code(X), px, ldx, _on(weight, "weight", (d,), torch.float32, device), r_dtype,
+        _on(residual, "residual", shape, residual.dtype if residual is not None else None, device),
+        _on(residual_out, "residual_out", shape, residual.dtype if residual is not None else None,
+            device),
+        eps, y_dtype, _on(Y, "Y", shape, Y.dtype, device), group, ps, _on_stream(stream, device)),
+        "ret_rms_norm")
+    return Y
+
+
+def ret_causal_conv(X, weight, Y, bias=None, swish=True, lengths=None, state_in=None,
+                    state_out=None, stream=None):
+    """Causal convolution of the rows X [B,L,D] (strided rows) with weight
+    [D,width] (and bias [D]) per channel, then the swish; Y [B,L,D].
+    state_in / state_out [B,width-1,D] hold the last inputs (one tensor for
+    both updates it in place; L = 1 is a single token), lengths [B] (int32) the
+    valid rows of a padded batch.  Returns (Y, state_out)."""
+    device = _device_of(X, "X")
+    B, L, D = X.shape
+    width = weight.shape[-1]
+    dt = X.dtype
+    px, ldx = _rows(X, "X", X.shape, dt, device)
+    held = (B, width - 1, D)
+    _check(load_library().ret_causal_conv(
+        B, L, D, width, _dtype_code(X), px, ldx, _on(weight, "weight", (D, width), torch.float32, device),
+        _on(bias, "bias", (D,), torch.float32, device), int(bool(swish)),
+        _on(lengths, "lengths", (B,), torch.int32, device), _on(state_in, "state_in", held, dt, device),
+        _on(state_out, "state_out", held, dt, device), _on(Y, "Y", X.shape, dt, device),
+        _on_stream(stream, device)), "ret_causal_conv")
+    return Y, state_out
+
+
+def ret_selective_scan(U, delta, A, Bm, Cm, Y, skip=None, Z=None, delta_bias=None, softplus=True,
+                       lengths=None, state_in=None, state_out=None, stream=None):
+    """Selective scan of U, delta (and gate Z) [B,L,D] (strided rows) with A
+    [D,N], Bm, Cm [B,L,G,N] or [B,L,N] (strided rows) into Y [B,L,D].
+    state_in / state_out [B,D,N] fp32 (one tensor for both updates it in place;
+    L = 1 is a single token), lengths [B] (int32) the valid rows of a padded
+    batch.  Returns (Y, state_out)."""
+    device = _device_of(U, "U")
+    shape, dt = U.shape, U.dtype
+    B, L, D = shape
+    N = A.shape[-1]
+    G = 1 if Bm.dim() == 3 else Bm.shape[2]
+    gn = (B, L, G * N)
+    flat = lambda t: t if t.dim() == 3 else t.flatten(2) if t.stride(2) == N or G == 1 else t  # noqa: E731
+    pu, ldu = _rows(U, "U", shape, dt, device)
+    pd, ldd = _rows(delta, "delta", shape, dt, device)
+    pz, ldz = (None, 0) if Z is None else _rows(Z, "Z", shape, dt, device)
+    pb, ldb = _rows(flat(Bm), "Bm", gn, dt, device)
+    pc, ldc = _rows(flat(Cm), "Cm", gn, dt, device)
+    held = (B, D, N)
+    desc = RetScanDesc(B, L, D, N, G, _dtype_code(U), int(bool(softplus)), ldu, ldd, ldz, ldb, ldc)
+    _check(load_library().ret_selective_scan(
+        desc, pu, pd, _on(delta_bias, "delta_bias", (D,), torch.float32, device),
+        _on(A, "A", (D, N), torch.float32, device), pb, pc,
+        _on(skip, "skip", (D,), torch.float32, device), pz,
+        _on(lengths, "lengths", (B,), torch.int32, device),
+        _on(state_in, "state_in", held, torch.float32, device),
+        _on(state_out, "state_out", held, torch.float32, device), _on(Y, "Y", shape, dt, device),
+        _on_stream(stream, device)), "ret_selective_scan")
+    return Y, state_out
+
+
+def ret_matvec_w4(X, Wq, scales, Y, zeros=None, x_scales=None, stream=None):
+    """Y [M,N] = X [M,K] (strided rows; float32, bfloat16, or int8 /
+    float8_e4m3fn codes with x_scales [M,groups]) times the 4-bit weights Wq
+    [N,K/2] (uint8) with scales [N,K/group] (bfloat16) and zeros (uint8, same
+    shape).  Returns Y."""
+    device = _device_of(X, "X")
+    M, K = X.shape
+    N, groups = scales.shape
+    x_dtype = _CODES.get(X.dtype)
+    if x_dtype is None:
+        raise TypeError(f"unsupported dtype {X.dtype}")
+    if groups < 1 or K % groups:
+        raise ValueError("scales must divide the columns into equal groups")
+    px, ldx = _rows(X, "X", X.shape, X.dtype, device)
+    x_group, xg = 0, None
+    if x_dtype >= RET_I8:
+        if x_scales is None:
+            raise ValueError("8-bit rows need x_scales")
+        n = x_scales.shape[-1]
+        if n < 1 or K % n:
+            raise ValueError("x_scales must divide the columns into equal groups")
+        x_group = 0 if n == 1 else K // n
+        xg = _on(x_scales, "x_scales", (M, n), torch.float32, device)
+    elif x_scales is not None:
+        raise ValueError("x_scales go with 8-bit rows")
+    _check(load_library().ret_matvec_w4(
+        M, N, K, K // groups, x_dtype, px, ldx, xg, x_group,
+        _on(Wq, "Wq", (N, K // 2), torch.uint8, device),
+        _on(scales, "scales", (N, groups), torch.bfloat16, device),
+        _on(zeros, "zeros", (N, groups), torch.uint8, device), _dtype_code(Y),
+        _on(Y, "Y", (M, N), Y.dtype, device), _on_stream(stream, device)), "ret_matvec_w4")
+    return Y
+
+
+def ret_quantize_w4(W, group, zeros=False, stream=None):
+    """4-bit codes of W [K,N] (strided rows) for ret_matvec_w4, with a scale (and,
+    with `zeros`, a zero point) per `group` rows of each column.  Returns
+    (Wq [N,K/2] uint8, scales [N,K/group] bfloat16, zeros uint8 or None)."""
+    device = _device_of(W, "W")
+    K, N = W.shape
+    pw, ldw = _rows(W, "W", W.shape, W.dtype, device)
+    wq = torch.empty(N, K // 2, device=W.device, dtype=torch.uint8)
+    groups = K // group if group > 0 else 0
+    scales = torch.empty(N, groups, device=W.device, dtype=torch.bfloat16)
+    zp = torch.empty(N, groups, device=W.device, dtype=torch.uint8) if zeros else None
+    _check(load_library().ret_quantize_w4(K, N, int(group), _dtype_code(W), pw, ldw, wq.data_ptr(),
+                                          scales.data_ptr(), None if zp is None else zp.data_ptr(),
+                                          _on_stream(stream, device)), "ret_quantize_w4")
+    return wq, scales, zp
 
 
 def ret_last_device_status(stream=None) -> int:
