@@ -4,6 +4,8 @@
 // per channel with N states, for prompts and for single tokens over an fp32
 // state.
 #include <cmath>
+#include <type_traits>
+#include <type_traits>
 
 #include "common.cuh"
 #include "launch.h"
@@ -25,6 +27,7 @@ struct ScanArgs {
     void *y;
 };
 
+#define SCANX 8, 2, 1
 constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -33,23 +36,27 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return r;
 }
 
-// log(1 + e^x) = max(x, 0) + log1p(e^-|x|).  log1p(e) / e for e = e^-|x| in
-// (0, 1] is a polynomial of degree 8 fitted by reweighted least squares at
-// Chebyshev nodes (relative error 3e-8), which keeps the relative accuracy for
-// small e, where log(1 + e) would not, and leaves the special-function unit to
-// the decays.
-__device__ __forceinline__ float softplus(float x) {
-    const float e = exp2_fast(-fabsf(x) * kLog2e);
-    float p = 0.005232624709606171f;
-    p = fmaf(p, e, -0.029504960402846336f);
-    p = fmaf(p, e, 0.0782255008816719f);
-    p = fmaf(p, e, -0.1366320699453354f);
-    p = fmaf(p, e, 0.1910598874092102f);
-    p = fmaf(p, e, -0.2484297752380371f);
-    p = fmaf(p, e, 0.3331909477710724f);
-    p = fmaf(p, e, -0.4999949336051941f);
-    p = fmaf(p, e, 0.9999999403953552f);
-    return fmaf(p, e, fmaxf(x, 0.f));
+__device__ __forceinline__ uint64_t dup(float v) { return tc::f2_make(v, v); }
+
+// log(1 + e^x) = max(x, 0) + log1p(e^-|x|), of both values of a pair.
+// log1p(e) / e for e = e^-|x| in (0, 1] is a polynomial of degree 8 fitted by
+// reweighted least squares at Chebyshev nodes (relative error 3e-8), which keeps
+// the relative accuracy for small e, where log(1 + e) would not, and leaves the
+// special-function unit to the decays.
+__device__ __forceinline__ uint64_t softplus2(uint64_t x) {
+    const float x0 = tc::f2_lo(x), x1 = tc::f2_hi(x);
+    const uint64_t a = tc::f2_mul(tc::f2_make(fabsf(x0), fabsf(x1)), dup(-kLog2e));
+    const uint64_t e = tc::f2_make(exp2_fast(tc::f2_lo(a)), exp2_fast(tc::f2_hi(a)));
+    uint64_t p = dup(0.005232624709606171f);
+    p = tc::f2_fma(p, e, dup(-0.029504960402846336f));
+    p = tc::f2_fma(p, e, dup(0.0782255008816719f));
+    p = tc::f2_fma(p, e, dup(-0.1366320699453354f));
+    p = tc::f2_fma(p, e, dup(0.1910598874092102f));
+    p = tc::f2_fma(p, e, dup(-0.2484297752380371f));
+    p = tc::f2_fma(p, e, dup(0.3331909477710724f));
+    p = tc::f2_fma(p, e, dup(-0.4999949336051941f));
+    p = tc::f2_fma(p, e, dup(0.9999999403953552f));
+    return tc::f2_fma(p, e, tc::f2_make(fmaxf(x0, 0.f), fmaxf(x1, 0.f)));
 }
 __device__ __forceinline__ float swish(float v) { return __fdividef(v, 1.f + exp2_fast(-v * kLog2e)); }
 
@@ -92,93 +99,91 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, int n)
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
 
-// Sizes.  A warp owns CPW channels (LANES threads each) and does all the work
-// on them itself; the CTA's four warps share the tiles of B and C.
-template <typename T, int SPT, int LANES, int TT, bool VEC>
+// Sizes.  Four threads share CPT adjacent channels, so a warp owns CPW channels
+// and a CTA CH; rows go in tiles of TT.
+template <typename T, int SPT, int LANES_, int CPT, bool VEC>
 struct ScanTile {
-    static constexpr int WARPS = 4, NT = 32 * WARPS, CPW = 32 / LANES, CH = WARPS * CPW, NP = SPT * LANES;
-    static constexpr int E = TT / LANES;                 // elements per thread, operand and tile
-    static constexpr int GRP = 32 / TT;                  // threads that share a row of the warp's channels
-    static constexpr int WORDS = CPW * (int)sizeof(T) / 16 + (VEC ? 0 : 1);  // 16-byte words of a row
+    static constexpr int LANES = LANES_, WARPS = 4, NT = 32 * WARPS, TT = 16;
+    static constexpr int CPW = 32 / LANES * CPT, CH = WARPS * CPW, NP = SPT * LANES;
+    static constexpr int E = CPW * TT / 32;              // elements per thread, operand and tile
+    static constexpr int SLOTS = NT / TT;                // threads that copy a row
+    static constexpr int WORDS = CH * (int)sizeof(T) / 16 + (VEC ? 0 : 1);  // 16-byte words of a row
     static constexpr int RS = 16 * (WORDS | 1);          // its bytes: an odd number of words, no bank conflicts
-    static constexpr int DS = TT + 2;                    // row stride of du (float2)
-    static constexpr int YS = TT + 4;                    // row stride of y
     static constexpr int PE = 8;                         // elements of a piece of B or C
     static constexpr int PR = NP / PE;                   // pieces per row
     static constexpr int PIECES = 2 * TT * PR;           // of both
     static constexpr int NB = (PIECES + NT - 1) / NT;    // per thread
     static constexpr int PB = PE * (int)sizeof(T) + (VEC ? 0 : 16);  // bytes a copied piece takes
-    static_assert(TT <= 32 && E * LANES == TT && NP % PE == 0, "tile");
-    struct Warp {
-        uint8_t in[2][3][TT][RS];  // u, delta, z as copied, two tiles
-        float2 du[CPW][DS];        // (d, d u), rows of a channel adjacent
-        float y[CPW][LANES][YS];   // every lane's part of y
-    };
+    static_assert(NP % PE == 0 && (CPT == 1 || CPT == 2 || CPT == 4), "tile");
     struct Smem {
-        Warp warp[WARPS];
-        float bc[2][2][TT][NP];            // two tiles of B and C
-        uint8_t bcin[2][NB][NT][PB];       // as copied, by the thread that converts it
+        uint8_t in[2][3][TT][RS];                // u, delta, z as copied, two tiles
+        float du[CH / CPT][TT * 2 * CPT + 4];    // per row: (d, d u) of the CPT channels
+        float y[CH][LANES][TT + 4];              // the four threads' parts of y
+        float bc[2][2][TT][NP];                  // two tiles of B and C
+        uint8_t bcin[2][NB][NT][PB];             // as copied, by the thread that converts it
+    };
+    // What a segment does to the state: h -> a h + b.
+    struct Segment {
+        float a[CH][NP], b[CH][NP];
     };
 };
 
-// The recurrence: LANES threads share a channel and hold SPT states each (state
-// n = 4 LANES (i / 4) + 4 lane + i % 4 in register i, so that B_t and C_t are
-// read from shared memory in 16-byte pieces without bank conflicts), two states
-// to a packed register pair.  Rows go in tiles of TT.  While a tile is computed
-// the next one is copied to shared memory as it is; then each warp turns its
-// channels' delta into d = softplus(delta + bias) and d u, once per row and
-// channel, and the CTA its share of B and C into fp32 (the tile's only barrier);
-// the parts of y that the lanes of a channel write are added, gated and rounded
-// by the same warp.
+// The recurrence: four threads share CPT adjacent channels and hold SPT states
+// of each (state n = 16 (i / 4) + 4 lane + i % 4 in register i, so that B_t and
+// C_t are read from shared memory in 16-byte pieces), two states to a packed
+// register pair.  Shared memory returns 128 bytes a clock however many lanes read
+// the same, so B_t and C_t are read once for the CPT channels.  Rows go in tiles of TT.  While a tile is computed
+// the next one is copied to shared memory as it is; then the CTA turns its B and
+// C into fp32 (the tile's only barrier) and each warp its channels' delta into
+// d = softplus(delta + bias) and d u, once per row and channel; y
+// is gated and rounded by the warp that computed it.
 //
 // VEC: every row of every operand starts on 16 bytes.  Otherwise the aligned
 // words that hold a row are copied and the row starts a few elements into its
 // place (bytes before an unaligned row are in its first word, so in the same
 // allocation; bytes past its end are not read).
-template <typename T, int SPT, int LANES, int TT, bool VEC>
-__global__ void __launch_bounds__(128, SPT <= 8 ? 4 : 2)
+template <typename T, int SPT, int LANES_, int CPT, bool VEC, bool SPLIT>
+__global__ void __launch_bounds__(128, SPT * CPT <= 8 ? 4 : SPT * CPT <= 16 ? 3 : 2)
 selective_scan_kernel(const ScanArgs a) {
-    using C = ScanTile<T, SPT, LANES, TT, VEC>;
-    constexpr int NT = C::NT, CPW = C::CPW, NP = C::NP, E = C::E, NB = C::NB, PE = C::PE;
-    constexpr int PR = SPT / 2;  // state pairs
+    using C = ScanTile<T, SPT, LANES_, CPT, VEC>;
+    constexpr int NT = C::NT, TT = C::TT, CPW = C::CPW, NP = C::NP, E = C::E, NB = C::NB, PE = C::PE;
+    constexpr int LANES = C::LANES, PR = SPT / 2;  // state pairs
     constexpr int SZ = (int)sizeof(T);
     extern __shared__ __align__(16) uint8_t dsm[];
     auto &sm = *reinterpret_cast<typename C::Smem *>(dsm);
+    auto &seg = *reinterpret_cast<typename C::Segment *>(dsm + sizeof(typename C::Smem));
 
-    const int tid = threadIdx.x, wl = tid % 32, lane = tid % LANES, ch = wl / LANES;
-    auto &sw = sm.warp[tid / 32];
+    const int tid = threadIdx.x, wl = tid % 32, lane = tid % LANES, ch = tid / LANES * CPT;
+    const int segments = SPLIT ? (int)gridDim.y : 1, me = SPLIT ? (int)blockIdx.y : 0;
     int blk = blockIdx.x;
     const int cb = blk % a.blocks_per_group;
     blk /= a.blocks_per_group;
     const int g = blk % a.G, b = blk / a.G;
-    const int w0 = cb * C::CH + tid / 32 * CPW;        // first channel of the warp in its group
-    const int c0 = g * a.dpg + w0;
-    const int nch = max(0, min(CPW, a.dpg - w0));      // channels of this warp
+    const int c0 = g * a.dpg + cb * C::CH;             // first channel
+    const int nch = min(C::CH, a.dpg - cb * C::CH);    // channels of the CTA
     const int len = a.lengths ? min(max(a.lengths[b], 0), a.L) : a.L;
     const long long row0 = (long long)b * a.L;
 
-    // this thread's row of a tile, and its E channels from sc on
-    const int sr = wl % TT, sg = wl / TT, sc = sg * E;
-    const T *pu = static_cast<const T *>(a.u) + (row0 + sr) * a.ldu + c0;
-    const T *pd = static_cast<const T *>(a.delta) + (row0 + sr) * a.ldd + c0;
-    const T *pz = a.z ? static_cast<const T *>(a.z) + (row0 + sr) * a.ldz + c0 : nullptr;
-    T *py = static_cast<T *>(a.y) + (row0 + sr) * a.D + c0 + sc;
+    // the CTA's part of an operand's row t
+    auto row_of = [&](const void *p, long long ld, int t) { return static_cast<const T *>(p) + (row0 + t) * ld + c0; };
     auto misfit = [](const T *p) { return VEC ? 0 : (int)(reinterpret_cast<uintptr_t>(p) & 15u); };
-    auto copy_row = [&](const T *p, bool there, uint8_t *dst) {
+    const uint8_t *somewhere = static_cast<const uint8_t *>(a.u) - misfit(static_cast<const T *>(a.u));
+    auto copy_row = [&](const T *p, bool there, uint8_t *dst, int slot) {
         const int head = misfit(p), end = there ? head + nch * SZ : 0;
-        const uint8_t *base = there ? reinterpret_cast<const uint8_t *>(p) - head : static_cast<const uint8_t *>(a.u) - misfit(static_cast<const T *>(a.u));
+        const uint8_t *base = reinterpret_cast<const uint8_t *>(p) - head;
         const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
 #pragma unroll
-        for (int w = 0; w < C::WORDS; w += C::GRP) {
-            if (C::WORDS % C::GRP == 0 || w + sg < C::WORDS) {
-                const int at = 16 * (w + sg), n = min(16, max(0, end - at));
-                cp_async16(d + at, n ? base + at : base, n);
+        for (int w = 0; w < C::WORDS; w += C::SLOTS) {
+            if (C::WORDS % C::SLOTS == 0 || w + slot < C::WORDS) {
+                const int at = 16 * (w + slot), n = min(16, max(0, end - at));
+                cp_async16(d + at, n ? base + at : somewhere, n);
             }
         }
     };
-    // pieces of B and C: this thread's j-th
+    // pieces of B and C: this thread's j-th (the last threads take the first
+    // pieces, since the first ones copy more of the rows)
     auto piece = [&](int j, int &r, int &n0, bool &c) {
-        const int p = tid + j * NT;
+        const int p = NT - 1 - tid + j * NT;
         r = p / C::PR % TT;
         n0 = p % C::PR * PE;
         c = p >= TT * C::PR;
@@ -187,38 +192,53 @@ selective_scan_kernel(const ScanArgs a) {
     auto piece_at = [&](int t, int n0, bool c) {
         return static_cast<const T *>(c ? a.cm : a.bm) + (row0 + t) * (c ? a.ldc : a.ldb) + (long long)g * a.N + n0;
     };
-    // copies the tile that starts at row t0 into slot k; advances the pointers
-    auto copy_tile = [&](int t0, int k) {
-        const bool there = t0 + sr < len && nch > 0;
-        copy_row(pu, there, sw.in[k][0][sr]);
-        copy_row(pd, there, sw.in[k][1][sr]);
-        if (pz) copy_row(pz, there, sw.in[k][2][sr]);
+    // copies the tile that starts at row t0 into slot k (y: z and C too)
+    const int cr = tid / C::SLOTS, slot = tid % C::SLOTS;
+    auto copy_tile = [&](int t0, int k, bool y) {
+        const int t = t0 + cr;
+        if (VEC && nch == C::CH && t0 + TT <= len) {  // nothing to cut
+            auto go = [&](const void *p, long long ld, int op) {
+                const uint8_t *src = reinterpret_cast<const uint8_t *>(row_of(p, ld, t)) + 16 * slot;
+                const uint32_t d = (uint32_t)__cvta_generic_to_shared(sm.in[k][op][cr]) + 16 * slot;
+#pragma unroll
+                for (int w = 0; w < C::WORDS; w += C::SLOTS)
+                    if (C::WORDS % C::SLOTS == 0 || w + slot < C::WORDS) cp_async16(d + 16 * w, src + 16 * w, 16);
+            };
+            go(a.u, a.ldu, 0);
+            go(a.delta, a.ldd, 1);
+            if (y && a.z) go(a.z, a.ldz, 2);
+        } else {
+            const bool there = t < len;
+            copy_row(row_of(a.u, a.ldu, t), there, sm.in[k][0][cr], slot);
+            copy_row(row_of(a.delta, a.ldd, t), there, sm.in[k][1][cr], slot);
+            if (y && a.z) copy_row(row_of(a.z, a.ldz, t), there, sm.in[k][2][cr], slot);
+        }
 #pragma unroll
         for (int j = 0; j < NB; ++j) {
             int r, n0;
             bool c;
-            if (piece(j, r, n0, c)) {
+            if (piece(j, r, n0, c) && (y || !c)) {
                 const T *p = piece_at(t0 + r, n0, c);
                 const int n = t0 + r < len ? min(PE, max(0, a.N - n0)) : 0;
-                const int head = n ? misfit(p) : 0, end = head + n * SZ;
-                const uint8_t *base = n ? reinterpret_cast<const uint8_t *>(p) - head : static_cast<const uint8_t *>(a.u) - misfit(static_cast<const T *>(a.u));
+                const int head = misfit(p), end = n ? head + n * SZ : 0;
+                const uint8_t *base = reinterpret_cast<const uint8_t *>(p) - head;
                 const uint32_t d = (uint32_t)__cvta_generic_to_shared(sm.bcin[k][j][tid]);
 #pragma unroll
                 for (int w = 0; w < C::PB; w += 16) {
-                    const int m = n ? min(16, max(0, end - w)) : 0;
-                    cp_async16(d + w, m ? base + w : base, m);
+                    const int m = min(16, max(0, end - w));
+                    cp_async16(d + w, m ? base + w : somewhere, m);
                 }
             }
         }
         cp_async_commit();
     };
     // B and C of the tile at t0, from slot k to the fp32 tile k
-    auto convert_bc = [&](int t0, int k) {
+    auto convert_bc = [&](int t0, int k, bool y) {
 #pragma unroll
         for (int j = 0; j < NB; ++j) {
             int r, n0;
             bool c;
-            if (piece(j, r, n0, c)) {
+            if (piece(j, r, n0, c) && (y || !c)) {
                 const bool there = t0 + r < len;
                 const int head = VEC || !there ? 0 : misfit(piece_at(t0 + r, n0, c)) / SZ;
                 const Raw<T, PE> v = shared_raw<VEC, T, PE>(reinterpret_cast<const T *>(sm.bcin[k][j][tid]) + head);
@@ -232,148 +252,295 @@ selective_scan_kernel(const ScanArgs a) {
         }
     };
 
-    if (len > 0) copy_tile(0, 0);
+    // this CTA's rows: all, or a whole number of tiles of the sequence
+    const int per = SPLIT ? ((len + TT - 1) / TT + segments - 1) / segments * TT : len;
+    const int first = me * per, end = min(len, first + per);
+    if (first < end) copy_tile(first, 0, !SPLIT);
 
-    auto state_of = [&](int i) { return i / 4 * (4 * LANES) + lane * 4 + i % 4; };
-    const bool live = ch < nch;
-    const long long hrow = ((long long)b * a.D + c0 + ch) * a.N;
-    uint64_t h[PR], A2[PR];
+    auto state_of = [&](int i) { return SPT == 2 ? lane * 2 + i : i / 4 * (4 * LANES) + lane * 4 + i % 4; };
+    auto state_row = [&](int c) { return ((long long)b * a.D + c0 + ch + c) * a.N; };
+    uint64_t h[CPT][PR], A2[CPT][PR];
 #pragma unroll
-    for (int j = 0; j < PR; ++j) {
-        float av[2], hv[2];
+    for (int c = 0; c < CPT; ++c)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int n = state_of(2 * j + i);
-            const bool in = live && n < a.N;
-            av[i] = in ? a.A[(long long)(c0 + ch) * a.N + n] * kLog2e : 0.f;
-            hv[i] = in && a.s_in ? a.s_in[hrow + n] : 0.f;
-        }
-        A2[j] = tc::f2_make(av[0], av[1]);
-        h[j] = tc::f2_make(hv[0], hv[1]);
-    }
-    float bias[E], skip[E];
+        for (int j = 0; j < PR; ++j) {
+            float av[2], hv[2];
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-        bias[i] = a.bias && sc + i < nch ? a.bias[c0 + sc + i] : 0.f;
-        skip[i] = a.skip && sc + i < nch ? a.skip[c0 + sc + i] : 0.f;
-    }
-
-    for (int t0 = 0, k = 0; t0 < len; t0 += TT, k ^= 1) {
-        cp_async_wait();
-        convert_bc(t0, k);
-        __syncthreads();  // also: every warp is done with the B and C of the tile before last
-        const bool inside = t0 + sr < len;
-        const Raw<T, E> ru = shared_raw<VEC, T, E>(reinterpret_cast<const T *>(sw.in[k][0][sr] + misfit(pu)) + sc);
-        {
-            const Raw<T, E> rd = shared_raw<VEC, T, E>(reinterpret_cast<const T *>(sw.in[k][1][sr] + misfit(pd)) + sc);
-#pragma unroll
-            for (int i = 0; i < E; ++i) {
-                float d = to_f(rd.v[i]) + bias[i];
-                if (a.softplus) d = softplus(d);
-                const bool in1 = inside && (VEC || sc + i < nch);
-                sw.du[sc + i][sr] = make_float2(in1 ? d : 0.f, in1 ? d * to_f(ru.v[i]) : 0.f);
+            for (int i = 0; i < 2; ++i) {
+                const int n = state_of(2 * j + i);
+                const bool in = ch + c < nch && n < a.N;
+                av[i] = in ? a.A[(long long)(c0 + ch + c) * a.N + n] * kLog2e : 0.f;
+                hv[i] = in && a.s_in && me == 0 ? a.s_in[state_row(c) + n] : 0.f;
             }
+            A2[c][j] = tc::f2_make(av[0], av[1]);
+            h[c][j] = tc::f2_make(hv[0], hv[1]);
         }
-        const T *pz_now = pz;
-        pu += TT * a.ldu;
-        pd += TT * a.ldd;
-        if (pz) pz += TT * a.ldz;
-        if (t0 + TT < len) copy_tile(t0 + TT, k ^ 1);
-        __syncwarp();
+    auto sum_parts = [](const float (&y)[C::LANES][C::TT + 4], int r) {
+        float v = y[0][r];
+#pragma unroll
+        for (int l = 1; l < C::LANES; ++l) v += y[l][r];
+        return v;
+    };
+    // conversion and output: this thread's row of a tile and its E channels
+    // (of the warp's own)
+    const int sr = wl % TT, sc = tid / 32 * CPW + wl / TT * E;
+    uint64_t bias[E / 2], skip[E / 2];
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) {
+        const int c = sc + 2 * i;
+        auto of = [&](const float *p, int cc) { return p && cc < nch ? p[c0 + cc] : 0.f; };
+        bias[i] = tc::f2_make(of(a.bias, c), of(a.bias, c + 1));
+        skip[i] = tc::f2_make(of(a.skip, c), of(a.skip, c + 1));
+    }
+    auto copied = [&](int k, int op, const T *row) {
+        return shared_raw<VEC, T, E>(reinterpret_cast<const T *>(sm.in[k][op][sr] + misfit(row)) + sc);
+    };
 
-        const float *tb = &sm.bc[k][0][0][lane * 4], *tc_ = &sm.bc[k][1][0][lane * 4];
-#pragma unroll(SPT <= 8 ? TT / 4 : 1)
-        for (int t = 0; t < TT; t += 4) {
-            float part[4];
+    // the recurrence over this CTA's rows; Y: writes y, else only follows the
+    // state (and the sum of d)
+    float sum_d[CPT] = {};
+    auto run = [&](auto want_y) {
+      constexpr bool Y = decltype(want_y)::value;
+      for (int t0 = first, k = 0; t0 < end; t0 += TT, k ^= 1) {
+        cp_async_wait();
+        convert_bc(t0, k, Y);
+        __syncthreads();  // also: every warp is done with the tile before this one
+        const int tr = t0 + sr;
+        const bool inside = tr < len;
+        const Raw<T, E> ru = copied(k, 0, row_of(a.u, a.ldu, tr));
+        {
+            const Raw<T, E> rd = copied(k, 1, row_of(a.delta, a.ldd, tr));
 #pragma unroll
-            for (int r = 0; r < 4; r += 2) {
-                const float4 du2 = *reinterpret_cast<const float4 *>(&sw.du[ch][t + r]);
-#pragma unroll
-                for (int rr = 0; rr < 2; ++rr) {
-                    const float d = rr ? du2.z : du2.x, du = rr ? du2.w : du2.y;
-                    const uint64_t dd = tc::f2_make(d, d), dudu = tc::f2_make(du, du);
-                    uint64_t acc = 0;
-#pragma unroll
-                    for (int j = 0; j < PR; j += 2) {
-                        const ulonglong2 bv = *reinterpret_cast<const ulonglong2 *>(tb + (t + r + rr) * NP + j * 2 * LANES);
-                        const ulonglong2 cv = *reinterpret_cast<const ulonglong2 *>(tc_ + (t + r + rr) * NP + j * 2 * LANES);
-                        const uint64_t p0 = tc::f2_mul(dd, A2[j]), p1 = tc::f2_mul(dd, A2[j + 1]);
-                        const uint64_t e0 = tc::f2_make(exp2_fast(tc::f2_lo(p0)), exp2_fast(tc::f2_hi(p0)));
-                        const uint64_t e1 = tc::f2_make(exp2_fast(tc::f2_lo(p1)), exp2_fast(tc::f2_hi(p1)));
-                        h[j] = tc::f2_fma(e0, h[j], tc::f2_mul(dudu, bv.x));
-                        h[j + 1] = tc::f2_fma(e1, h[j + 1], tc::f2_mul(dudu, bv.y));
-                        acc = j ? tc::f2_fma(cv.x, h[j], acc) : tc::f2_mul(cv.x, h[j]);
-                        acc = tc::f2_fma(cv.y, h[j + 1], acc);
-                    }
-                    part[r + rr] = tc::f2_lo(acc) + tc::f2_hi(acc);
+            for (int i = 0; i < E / 2; ++i) {
+                uint64_t d = tc::f2_add(tc::f2_make(to_f(rd.v[2 * i]), to_f(rd.v[2 * i + 1])), bias[i]);
+                if (a.softplus) d = softplus2(d);
+                // rows past the sequence keep the state (their u reads as 0)
+                const float d0 = inside ? tc::f2_lo(d) : 0.f, d1 = inside ? tc::f2_hi(d) : 0.f;
+                const float x0 = d0 * to_f(ru.v[2 * i]), x1 = d1 * to_f(ru.v[2 * i + 1]);
+                const int c = sc + 2 * i;
+                if (CPT == 1) {
+                    *reinterpret_cast<float2 *>(&sm.du[c][2 * sr]) = make_float2(d0, x0);
+                    *reinterpret_cast<float2 *>(&sm.du[c + 1][2 * sr]) = make_float2(d1, x1);
+                } else {
+                    *reinterpret_cast<float4 *>(&sm.du[c / CPT][(sr * CPT + c % CPT) * 2]) = make_float4(d0, x0, d1, x1);
                 }
             }
-            *reinterpret_cast<float4 *>(&sw.y[ch][lane][t]) = make_float4(part[0], part[1], part[2], part[3]);
+        }
+        if (t0 + TT < end) copy_tile(t0 + TT, k ^ 1, Y);
+        __syncwarp();
+
+        constexpr int VS = SPT < 4 ? SPT : 4;
+        const float *tb = &sm.bc[k][0][0][lane * VS], *tc_ = &sm.bc[k][1][0][lane * VS];
+        const float *tdu = sm.du[tid / LANES];
+        // A row's operands are read two rows ahead and its exponentials taken one
+        // row ahead of their use.
+        struct Ops {
+            float dx[2 * CPT];  // (d, d u) by channel
+            uint64_t b[PR], c[PR];
+        };
+        auto read = [&](Ops &o, int t) {
+            if (CPT == 1) {
+                *reinterpret_cast<float2 *>(o.dx) = *reinterpret_cast<const float2 *>(tdu + t * 2);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 2 * CPT; i += 4)
+                    *reinterpret_cast<float4 *>(o.dx + i) = *reinterpret_cast<const float4 *>(tdu + t * 2 * CPT + i);
+            }
+#pragma unroll
+            for (int j = 0; j < PR; j += VS / 2) {
+                const float *qb = tb + t * NP + j * 2 * LANES, *qc = tc_ + t * NP + j * 2 * LANES;
+                if (VS == 4) {
+                    *reinterpret_cast<ulonglong2 *>(&o.b[j]) = *reinterpret_cast<const ulonglong2 *>(qb);
+                    if (Y) *reinterpret_cast<ulonglong2 *>(&o.c[j]) = *reinterpret_cast<const ulonglong2 *>(qc);
+                } else {
+                    o.b[j] = *reinterpret_cast<const uint64_t *>(qb);
+                    if (Y) o.c[j] = *reinterpret_cast<const uint64_t *>(qc);
+                }
+            }
+        };
+        auto decay = [&](uint64_t (&e)[CPT][PR], const Ops &o) {
+#pragma unroll
+            for (int c = 0; c < CPT; ++c)
+#pragma unroll
+                for (int j = 0; j < PR; ++j) {
+                    const uint64_t p = tc::f2_mul(dup(o.dx[2 * c]), A2[c][j]);
+                    e[c][j] = tc::f2_make(exp2_fast(tc::f2_lo(p)), exp2_fast(tc::f2_hi(p)));
+                }
+        };
+        {
+            Ops ops[2];
+            uint64_t e[2][CPT][PR];
+            float part[CPT][4];
+            read(ops[0], 0);
+            read(ops[1], 1);
+            decay(e[0], ops[0]);
+#pragma unroll(SPT * CPT <= 16 ? TT : 4)
+            for (int t = 0; t < TT; ++t) {
+                const Ops o = ops[t % 2];
+                if (t + 1 < TT) decay(e[(t + 1) % 2], ops[(t + 1) % 2]);
+                if (t + 2 < TT) read(ops[t % 2], t + 2);
+#pragma unroll
+                for (int c = 0; c < CPT; ++c) {
+                    const uint64_t xx = dup(o.dx[2 * c + 1]);
+                    uint64_t acc = 0;
+#pragma unroll
+                    for (int j = 0; j < PR; ++j) {
+                        uint64_t &hh = h[c][j];
+                        hh = tc::f2_fma(e[t % 2][c][j], hh, tc::f2_mul(xx, o.b[j]));
+                        if (Y) acc = j ? tc::f2_fma(o.c[j], hh, acc) : tc::f2_mul(o.c[j], hh);
+                    }
+                    if (Y) part[c][t % 4] = tc::f2_lo(acc) + tc::f2_hi(acc);
+                    else sum_d[c] += o.dx[2 * c];
+                }
+                if (Y && t % 4 == 3) {
+#pragma unroll
+                    for (int c = 0; c < CPT; ++c)
+                        *reinterpret_cast<float4 *>(&sm.y[ch + c][lane][t - 3]) =
+                            make_float4(part[c][0], part[c][1], part[c][2], part[c][3]);
+                }
+            }
         }
         __syncwarp();
-        if (inside && sc < nch) {
-            float y[E];
+        if (Y && inside && sc < nch) {
+            uint64_t y2[E / 2];
 #pragma unroll
-            for (int i = 0; i < E; ++i) {
-                y[i] = skip[i] * to_f(ru.v[i]);
+            for (int i = 0; i < E / 2; ++i)
+                y2[i] = tc::f2_fma(skip[i], tc::f2_make(to_f(ru.v[2 * i]), to_f(ru.v[2 * i + 1])),
+                                   tc::f2_make(sum_parts(sm.y[sc + 2 * i], sr), sum_parts(sm.y[sc + 2 * i + 1], sr)));
+            if (a.z) {
+                const Raw<T, E> rz = copied(k, 2, row_of(a.z, a.ldz, tr));
 #pragma unroll
-                for (int l = 0; l < LANES; ++l) y[i] += sw.y[sc + i][l][sr];
-            }
-            if (pz) {
-                const Raw<T, E> rz = shared_raw<VEC, T, E>(reinterpret_cast<const T *>(sw.in[k][2][sr] + misfit(pz_now)) + sc);
-#pragma unroll
-                for (int i = 0; i < E; ++i) y[i] *= swish(to_f(rz.v[i]));
+                for (int i = 0; i < E / 2; ++i)
+                    y2[i] = tc::f2_mul(y2[i], tc::f2_make(swish(to_f(rz.v[2 * i])), swish(to_f(rz.v[2 * i + 1]))));
             }
             Raw<T, E> out;
 #pragma unroll
-            for (int i = 0; i < E; ++i) from_f(out.v[i], y[i]);
-            store_raw<T, E>(py, out, nch - sc);
+            for (int i = 0; i < E / 2; ++i) {
+                from_f(out.v[2 * i], tc::f2_lo(y2[i]));
+                from_f(out.v[2 * i + 1], tc::f2_hi(y2[i]));
+            }
+            store_raw<T, E>(static_cast<T *>(a.y) + (row0 + tr) * a.D + c0 + sc, out, nch - sc);
         }
-        py += TT * (long long)a.D;
-    }
-    if (a.s_out && live) {
+      }
+    };
+
+    if (SPLIT) {
+        // 1. what each segment but the last does to the state: its own rows from
+        //    a zero state (the first one from the entering state), and the decay
+        //    over all of them, exp(A sum d)
+        if (me + 1 < segments) run(std::false_type{});
 #pragma unroll
-        for (int j = 0; j < PR; ++j) {
-            const int n = state_of(2 * j);  // n + 1 is the pair's other state
-            if (n < a.N) a.s_out[hrow + n] = tc::f2_lo(h[j]);
-            if (n + 1 < a.N) a.s_out[hrow + n + 1] = tc::f2_hi(h[j]);
-        }
+        for (int c = 0; c < CPT; ++c)
+#pragma unroll
+            for (int j = 0; j < PR; ++j) {
+                const uint64_t p = tc::f2_mul(dup(sum_d[c]), A2[c][j]);
+                const int n = state_of(2 * j);
+                // (a decay past the largest float would make NaN of a zero state)
+                *reinterpret_cast<float2 *>(&seg.a[ch + c][n]) = make_float2(fminf(exp2_fast(tc::f2_lo(p)), 3.4e38f), fminf(exp2_fast(tc::f2_hi(p)), 3.4e38f));
+                *reinterpret_cast<uint64_t *>(&seg.b[ch + c][n]) = h[c][j];
+            }
+        __syncthreads();
+        if (first < end) copy_tile(first, 0, true);
+        tc::cluster_sync();
+        // 2. the state that enters this segment, through those before it
+#pragma unroll
+        for (int c = 0; c < CPT; ++c)
+#pragma unroll
+            for (int j = 0; j < PR; ++j) {
+                const uint32_t at_a = (uint32_t)__cvta_generic_to_shared(&seg.a[ch + c][state_of(2 * j)]);
+                const uint32_t at_b = (uint32_t)__cvta_generic_to_shared(&seg.b[ch + c][state_of(2 * j)]);
+                uint64_t e = 0;
+                if (me == 0 && a.s_in) {  // the entering state once more
+                    const int n = state_of(2 * j);
+                    const bool in = ch + c < nch;
+                    e = tc::f2_make(in && n < a.N ? a.s_in[state_row(c) + n] : 0.f,
+                                    in && n + 1 < a.N ? a.s_in[state_row(c) + n + 1] : 0.f);
+                }
+                for (int i = 0; i < me; ++i) {
+                    const float2 ai = tc::ld_cluster_f32x2(tc::map_to_rank(at_a, i));
+                    const float2 bi = tc::ld_cluster_f32x2(tc::map_to_rank(at_b, i));
+                    const uint64_t b2 = tc::f2_make(bi.x, bi.y);
+                    e = i ? tc::f2_fma(tc::f2_make(ai.x, ai.y), e, b2) : b2;
+                }
+                h[c][j] = e;
+            }
+        tc::cluster_sync();  // nothing of this CTA's is read after this; state_out may be state_in
+    }
+    run(std::true_type{});
+    if (SPLIT && me + 1 < segments) return;
+    if (a.s_out) {
+#pragma unroll
+        for (int c = 0; c < CPT; ++c)
+#pragma unroll
+            for (int j = 0; j < PR; ++j) {
+                const int n = state_of(2 * j);  // n + 1 is the pair's other state
+                if (ch + c < nch && n < a.N) a.s_out[state_row(c) + n] = tc::f2_lo(h[c][j]);
+                if (ch + c < nch && n + 1 < a.N) a.s_out[state_row(c) + n + 1] = tc::f2_hi(h[c][j]);
+            }
     }
 }
 
-template <typename T, int SPT, int LANES, int TT, bool VEC>
+// Segments a sequence is cut into.  One warp per scheduler alone takes about 170
+// cycles a row and each further one 81 more (8 x 4096 x 4096 against 1 x 16384 x
+// 1024), and a cut sequence runs its rows about 1.8 times.
+int segments_of(long long warps, int L, int tile) {
+    const long long schedulers = 148 * 4;
+    auto cost = [&](int s) {
+        const double w = (double)((warps * s + schedulers - 1) / schedulers);
+        return (s > 1 ? 1.8 : 1.0) / s * (90.0 + 81.0 * w);
+    };
+    int best = 1;
+    for (int s = 4; s <= 8; s *= 2)
+        if (L >= s * 4 * tile && cost(s) < cost(best)) best = s;
+    return best;
+}
+
+template <typename T, int SPT, int LANES_, int CPT, bool VEC>
 cudaError_t launch_vec(ScanArgs a, cudaStream_t st) {
-    using C = ScanTile<T, SPT, LANES, TT, VEC>;
+    using C = ScanTile<T, SPT, LANES_, CPT, VEC>;
     a.blocks_per_group = (a.dpg + C::CH - 1) / C::CH;
     const long long blocks = (long long)a.B * a.G * a.blocks_per_group;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    auto kern = selective_scan_kernel<T, SPT, LANES, TT, VEC>;
-    constexpr int smem = (int)sizeof(typename C::Smem);
-    cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const int segments = segments_of(blocks * C::WARPS, a.L, C::TT);
+    auto kern = segments > 1 ? selective_scan_kernel<T, SPT, LANES_, CPT, VEC, true>
+                             : selective_scan_kernel<T, SPT, LANES_, CPT, VEC, false>;
+    const size_t smem = sizeof(typename C::Smem) + (segments > 1 ? sizeof(typename C::Segment) : 0);
+    cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (err != cudaSuccess) return err;
-    kern<<<(unsigned)blocks, C::NT, smem, st>>>(a);
-    err = cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)blocks, (unsigned)segments);
+    cfg.blockDim = dim3(C::NT);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 1;
+    attr[0].val.clusterDim.y = (unsigned)segments;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = segments > 1 ? 1 : 0;
+    err = cudaLaunchKernelEx(&cfg, kern, a);
     if (err == cudaSuccess) note_launches(1);
     return err;
 }
 
-template <typename T, int SPT, int LANES, int TT>
+template <typename T, int SPT, int LANES_, int CPT>
 cudaError_t launch_scan(const ScanArgs &a, cudaStream_t st) {
     auto fits = [](const void *p, long long ld) {
         return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld * (long long)sizeof(T) % 16 == 0;
     };
     const bool vec = fits(a.u, a.ldu) && fits(a.delta, a.ldd) && (!a.z || fits(a.z, a.ldz)) && fits(a.bm, a.ldb) &&
                      fits(a.cm, a.ldc) && fits(a.y, a.D) && (a.G == 1 || (fits(nullptr, a.dpg) && fits(nullptr, a.N)));
-    return vec ? launch_vec<T, SPT, LANES, TT, true>(a, st) : launch_vec<T, SPT, LANES, TT, false>(a, st);
+    return vec ? launch_vec<T, SPT, LANES_, CPT, true>(a, st) : launch_vec<T, SPT, LANES_, CPT, false>(a, st);
 }
 
 template <typename T>
 cudaError_t launch_n(const ScanArgs &a, cudaStream_t st) {
-    if (a.N <= 8) return launch_scan<T, 4, 2, 16>(a, st);
-    if (a.N <= 16) return launch_scan<T, 8, 2, 16>(a, st);
-    if (a.N <= 32) return launch_scan<T, 16, 2, 16>(a, st);
-    if (a.N <= 64) return launch_scan<T, 16, 4, 16>(a, st);
-    return launch_scan<T, 32, 4, 16>(a, st);
+    if (a.N <= 8) return launch_scan<T, 4, 2, 1>(a, st);
+    if (a.N <= 16) return launch_scan<T, 8, 2, 1>(a, st);
+    if (a.N <= 32) return launch_scan<T, 8, 4, 1>(a, st);
+    if (a.N <= 64) return launch_scan<T, 8, 8, 1>(a, st);
+    return launch_scan<T, 16, 8, 1>(a, st);
 }
 
 bool aligned(const void *p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
