@@ -27,7 +27,6 @@ struct ScanArgs {
     void *y;
 };
 
-#define SCANX 8, 2, 1
 constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -99,12 +98,12 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, int n)
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
 
-// Sizes.  Four threads share CPT adjacent channels, so a warp owns CPW channels
-// and a CTA CH; rows go in tiles of TT.
-template <typename T, int SPT, int LANES_, int CPT, bool VEC>
+// Sizes.  LANES threads share a channel and hold SPT states each, so a warp owns
+// CPW channels and a CTA CH; rows go in tiles of TT.
+template <typename T, int SPT, int LANES, bool VEC>
 struct ScanTile {
-    static constexpr int LANES = LANES_, WARPS = 4, NT = 32 * WARPS, TT = 16;
-    static constexpr int CPW = 32 / LANES * CPT, CH = WARPS * CPW, NP = SPT * LANES;
+    static constexpr int WARPS = 4, NT = 32 * WARPS, TT = 16;
+    static constexpr int CPW = 32 / LANES, CH = WARPS * CPW, NP = SPT * LANES;
     static constexpr int E = CPW * TT / 32;              // elements per thread, operand and tile
     static constexpr int SLOTS = NT / TT;                // threads that copy a row
     static constexpr int WORDS = CH * (int)sizeof(T) / 16 + (VEC ? 0 : 1);  // 16-byte words of a row
@@ -114,11 +113,11 @@ struct ScanTile {
     static constexpr int PIECES = 2 * TT * PR;           // of both
     static constexpr int NB = (PIECES + NT - 1) / NT;    // per thread
     static constexpr int PB = PE * (int)sizeof(T) + (VEC ? 0 : 16);  // bytes a copied piece takes
-    static_assert(NP % PE == 0 && (CPT == 1 || CPT == 2 || CPT == 4), "tile");
+    static_assert(NP % PE == 0 && E >= 2, "tile");
     struct Smem {
         uint8_t in[2][3][TT][RS];                // u, delta, z as copied, two tiles
-        float du[CH / CPT][TT * 2 * CPT + 4];    // per row: (d, d u) of the CPT channels
-        float y[CH][LANES][TT + 4];              // the four threads' parts of y
+        float2 du[CH][TT + 2];                   // (d, d u)
+        float y[CH][LANES][TT + 4];              // its threads' parts of y
         float bc[2][2][TT][NP];                  // two tiles of B and C
         uint8_t bcin[2][NB][NT][PB];             // as copied, by the thread that converts it
     };
@@ -128,32 +127,46 @@ struct ScanTile {
     };
 };
 
-// The recurrence: four threads share CPT adjacent channels and hold SPT states
-// of each (state n = 16 (i / 4) + 4 lane + i % 4 in register i, so that B_t and
-// C_t are read from shared memory in 16-byte pieces), two states to a packed
-// register pair.  Shared memory returns 128 bytes a clock however many lanes read
-// the same, so B_t and C_t are read once for the CPT channels.  Rows go in tiles of TT.  While a tile is computed
-// the next one is copied to shared memory as it is; then the CTA turns its B and
-// C into fp32 (the tile's only barrier) and each warp its channels' delta into
-// d = softplus(delta + bias) and d u, once per row and channel; y
-// is gated and rounded by the warp that computed it.
+// The recurrence: LANES threads share a channel and hold SPT states each (state
+// n = 4 LANES (i / 4) + 4 lane + i % 4 in register i, so that B_t and C_t are read
+// from shared memory in 16-byte pieces), two states to a packed register pair.
+// Rows go in tiles of TT.  While a tile is computed the next one is copied to
+// shared memory as it is; then the CTA turns its B and C into fp32 (the tile's only
+// barrier) and each warp its channels' delta into d = softplus(delta + bias) and
+// d u, once per row and channel; y is gated and rounded by the warp that computed
+// it.
+//
+// What bounds it: N exponentials per row and channel on the special-function
+// units (16 a clock and SM), 478 us for 8 x 4096 rows of 4096 channels with 16
+// states, next to some 60 instructions a row for a warp's 16 channels and the reads
+// of B and C, which return 128 bytes a clock however many lanes read the same.
+// Measured 869 us there, 165 us being the floor of its bytes.  Measured and not
+// kept: 4 threads a channel (942 us; 1085 with one register pair of du in place of
+// two copies), 2 channels a thread (945), a polynomial for a quarter of the
+// exponentials (991), unpacked arithmetic (992): what costs is instructions and
+// shared memory as much as the exponentials, and 2048 warps are 3.5 a scheduler,
+// of which the fullest have 4.
+//
+// SPLIT (few channels): a cluster of CTAs shares the channels, each CTA one segment
+// of the rows.  1 x 16384 rows of 1024 channels: 1462 us in one piece, 443 in 8
+// segments, 314 in 16.
 //
 // VEC: every row of every operand starts on 16 bytes.  Otherwise the aligned
 // words that hold a row are copied and the row starts a few elements into its
 // place (bytes before an unaligned row are in its first word, so in the same
 // allocation; bytes past its end are not read).
-template <typename T, int SPT, int LANES_, int CPT, bool VEC, bool SPLIT>
-__global__ void __launch_bounds__(128, SPT * CPT <= 8 ? 4 : SPT * CPT <= 16 ? 3 : 2)
+template <typename T, int SPT, int LANES, bool VEC, bool SPLIT>
+__global__ void __launch_bounds__(128, SPT <= 8 ? 4 : 3)
 selective_scan_kernel(const ScanArgs a) {
-    using C = ScanTile<T, SPT, LANES_, CPT, VEC>;
+    using C = ScanTile<T, SPT, LANES, VEC>;
     constexpr int NT = C::NT, TT = C::TT, CPW = C::CPW, NP = C::NP, E = C::E, NB = C::NB, PE = C::PE;
-    constexpr int LANES = C::LANES, PR = SPT / 2;  // state pairs
+    constexpr int PR = SPT / 2;  // state pairs
     constexpr int SZ = (int)sizeof(T);
     extern __shared__ __align__(16) uint8_t dsm[];
     auto &sm = *reinterpret_cast<typename C::Smem *>(dsm);
     auto &seg = *reinterpret_cast<typename C::Segment *>(dsm + sizeof(typename C::Smem));
 
-    const int tid = threadIdx.x, wl = tid % 32, lane = tid % LANES, ch = tid / LANES * CPT;
+    const int tid = threadIdx.x, wl = tid % 32, lane = tid % LANES, ch = tid / LANES;
     const int segments = SPLIT ? (int)gridDim.y : 1, me = SPLIT ? (int)blockIdx.y : 0;
     int blk = blockIdx.x;
     const int cb = blk % a.blocks_per_group;
@@ -257,28 +270,25 @@ selective_scan_kernel(const ScanArgs a) {
     const int first = me * per, end = min(len, first + per);
     if (first < end) copy_tile(first, 0, !SPLIT);
 
-    auto state_of = [&](int i) { return SPT == 2 ? lane * 2 + i : i / 4 * (4 * LANES) + lane * 4 + i % 4; };
-    auto state_row = [&](int c) { return ((long long)b * a.D + c0 + ch + c) * a.N; };
-    uint64_t h[CPT][PR], A2[CPT][PR];
+    auto state_of = [&](int i) { return i / 4 * (4 * LANES) + lane * 4 + i % 4; };
+    const long long state_row = ((long long)b * a.D + c0 + ch) * a.N;
+    auto entering = [&](int j) {  // states 2j and 2j + 1 before the first row
+        const int n = state_of(2 * j);
+        const bool in = a.s_in && ch < nch;
+        return tc::f2_make(in && n < a.N ? a.s_in[state_row + n] : 0.f, in && n + 1 < a.N ? a.s_in[state_row + n + 1] : 0.f);
+    };
+    uint64_t h[PR], A2[PR];
 #pragma unroll
-    for (int c = 0; c < CPT; ++c)
-#pragma unroll
-        for (int j = 0; j < PR; ++j) {
-            float av[2], hv[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int n = state_of(2 * j + i);
-                const bool in = ch + c < nch && n < a.N;
-                av[i] = in ? a.A[(long long)(c0 + ch + c) * a.N + n] * kLog2e : 0.f;
-                hv[i] = in && a.s_in && me == 0 ? a.s_in[state_row(c) + n] : 0.f;
-            }
-            A2[c][j] = tc::f2_make(av[0], av[1]);
-            h[c][j] = tc::f2_make(hv[0], hv[1]);
-        }
-    auto sum_parts = [](const float (&y)[C::LANES][C::TT + 4], int r) {
+    for (int j = 0; j < PR; ++j) {
+        const int n = state_of(2 * j);
+        const float *p = a.A + (long long)(c0 + ch) * a.N + n;
+        A2[j] = tc::f2_make(ch < nch && n < a.N ? p[0] * kLog2e : 0.f, ch < nch && n + 1 < a.N ? p[1] * kLog2e : 0.f);
+        h[j] = me == 0 ? entering(j) : 0;
+    }
+    auto sum_parts = [](const float (&y)[LANES][TT + 4], int r) {
         float v = y[0][r];
 #pragma unroll
-        for (int l = 1; l < C::LANES; ++l) v += y[l][r];
+        for (int l = 1; l < LANES; ++l) v += y[l][r];
         return v;
     };
     // conversion and output: this thread's row of a tile and its E channels
@@ -296,19 +306,18 @@ selective_scan_kernel(const ScanArgs a) {
         return shared_raw<VEC, T, E>(reinterpret_cast<const T *>(sm.in[k][op][sr] + misfit(row)) + sc);
     };
 
-    // the recurrence over this CTA's rows; Y: writes y, else only follows the
-    // state (and the sum of d)
-    float sum_d[CPT] = {};
+    // The recurrence over this CTA's rows.  Y: writes y; else only follows the
+    // state, and the sum of d (by tiles, so that long sums stay exact).
+    float sum_d = 0.f;
     auto run = [&](auto want_y) {
-      constexpr bool Y = decltype(want_y)::value;
-      for (int t0 = first, k = 0; t0 < end; t0 += TT, k ^= 1) {
-        cp_async_wait();
-        convert_bc(t0, k, Y);
-        __syncthreads();  // also: every warp is done with the tile before this one
-        const int tr = t0 + sr;
-        const bool inside = tr < len;
-        const Raw<T, E> ru = copied(k, 0, row_of(a.u, a.ldu, tr));
-        {
+        constexpr bool Y = decltype(want_y)::value;
+        for (int t0 = first, k = 0; t0 < end; t0 += TT, k ^= 1) {
+            cp_async_wait();
+            convert_bc(t0, k, Y);
+            __syncthreads();  // also: every warp is done with the tile before this one
+            const int tr = t0 + sr;
+            const bool inside = tr < len;
+            const Raw<T, E> ru = copied(k, 0, row_of(a.u, a.ldu, tr));
             const Raw<T, E> rd = copied(k, 1, row_of(a.delta, a.ldd, tr));
 #pragma unroll
             for (int i = 0; i < E / 2; ++i) {
@@ -316,112 +325,84 @@ selective_scan_kernel(const ScanArgs a) {
                 if (a.softplus) d = softplus2(d);
                 // rows past the sequence keep the state (their u reads as 0)
                 const float d0 = inside ? tc::f2_lo(d) : 0.f, d1 = inside ? tc::f2_hi(d) : 0.f;
-                const float x0 = d0 * to_f(ru.v[2 * i]), x1 = d1 * to_f(ru.v[2 * i + 1]);
-                const int c = sc + 2 * i;
-                if (CPT == 1) {
-                    *reinterpret_cast<float2 *>(&sm.du[c][2 * sr]) = make_float2(d0, x0);
-                    *reinterpret_cast<float2 *>(&sm.du[c + 1][2 * sr]) = make_float2(d1, x1);
-                } else {
-                    *reinterpret_cast<float4 *>(&sm.du[c / CPT][(sr * CPT + c % CPT) * 2]) = make_float4(d0, x0, d1, x1);
-                }
+                sm.du[sc + 2 * i][sr] = make_float2(d0, d0 * to_f(ru.v[2 * i]));
+                sm.du[sc + 2 * i + 1][sr] = make_float2(d1, d1 * to_f(ru.v[2 * i + 1]));
             }
-        }
-        if (t0 + TT < end) copy_tile(t0 + TT, k ^ 1, Y);
-        __syncwarp();
+            if (t0 + TT < end) copy_tile(t0 + TT, k ^ 1, Y);
+            __syncwarp();
 
-        constexpr int VS = SPT < 4 ? SPT : 4;
-        const float *tb = &sm.bc[k][0][0][lane * VS], *tc_ = &sm.bc[k][1][0][lane * VS];
-        const float *tdu = sm.du[tid / LANES];
-        // A row's operands are read two rows ahead and its exponentials taken one
-        // row ahead of their use.
-        struct Ops {
-            float dx[2 * CPT];  // (d, d u) by channel
-            uint64_t b[PR], c[PR];
-        };
-        auto read = [&](Ops &o, int t) {
-            if (CPT == 1) {
-                *reinterpret_cast<float2 *>(o.dx) = *reinterpret_cast<const float2 *>(tdu + t * 2);
-            } else {
+            // A row's operands are read two rows ahead and its exponentials taken
+            // one row ahead of their use.
+            struct Ops {
+                float2 dx;  // (d, d u)
+                uint64_t b[PR], c[PR];
+            };
+            const float *tb = &sm.bc[k][0][0][lane * 4], *tc_ = &sm.bc[k][1][0][lane * 4];
+            auto read = [&](Ops &o, int t) {
+                o.dx = sm.du[ch][t];
 #pragma unroll
-                for (int i = 0; i < 2 * CPT; i += 4)
-                    *reinterpret_cast<float4 *>(o.dx + i) = *reinterpret_cast<const float4 *>(tdu + t * 2 * CPT + i);
-            }
-#pragma unroll
-            for (int j = 0; j < PR; j += VS / 2) {
-                const float *qb = tb + t * NP + j * 2 * LANES, *qc = tc_ + t * NP + j * 2 * LANES;
-                if (VS == 4) {
-                    *reinterpret_cast<ulonglong2 *>(&o.b[j]) = *reinterpret_cast<const ulonglong2 *>(qb);
-                    if (Y) *reinterpret_cast<ulonglong2 *>(&o.c[j]) = *reinterpret_cast<const ulonglong2 *>(qc);
-                } else {
-                    o.b[j] = *reinterpret_cast<const uint64_t *>(qb);
-                    if (Y) o.c[j] = *reinterpret_cast<const uint64_t *>(qc);
+                for (int j = 0; j < PR; j += 2) {
+                    const int at = t * NP + j * 2 * LANES;
+                    *reinterpret_cast<ulonglong2 *>(&o.b[j]) = *reinterpret_cast<const ulonglong2 *>(tb + at);
+                    if (Y) *reinterpret_cast<ulonglong2 *>(&o.c[j]) = *reinterpret_cast<const ulonglong2 *>(tc_ + at);
                 }
-            }
-        };
-        auto decay = [&](uint64_t (&e)[CPT][PR], const Ops &o) {
-#pragma unroll
-            for (int c = 0; c < CPT; ++c)
+            };
+            auto decay = [&](uint64_t (&e)[PR], const Ops &o) {
 #pragma unroll
                 for (int j = 0; j < PR; ++j) {
-                    const uint64_t p = tc::f2_mul(dup(o.dx[2 * c]), A2[c][j]);
-                    e[c][j] = tc::f2_make(exp2_fast(tc::f2_lo(p)), exp2_fast(tc::f2_hi(p)));
+                    const uint64_t p = tc::f2_mul(dup(o.dx.x), A2[j]);
+                    e[j] = tc::f2_make(exp2_fast(tc::f2_lo(p)), exp2_fast(tc::f2_hi(p)));
                 }
-        };
-        {
+            };
             Ops ops[2];
-            uint64_t e[2][CPT][PR];
-            float part[CPT][4];
+            uint64_t e[2][PR];
+            float part[4], tile_d = 0.f;
             read(ops[0], 0);
             read(ops[1], 1);
             decay(e[0], ops[0]);
-#pragma unroll(SPT * CPT <= 16 ? TT : 4)
+#pragma unroll
             for (int t = 0; t < TT; ++t) {
                 const Ops o = ops[t % 2];
                 if (t + 1 < TT) decay(e[(t + 1) % 2], ops[(t + 1) % 2]);
                 if (t + 2 < TT) read(ops[t % 2], t + 2);
+                const uint64_t xx = dup(o.dx.y);
+                uint64_t acc = 0;
 #pragma unroll
-                for (int c = 0; c < CPT; ++c) {
-                    const uint64_t xx = dup(o.dx[2 * c + 1]);
-                    uint64_t acc = 0;
-#pragma unroll
-                    for (int j = 0; j < PR; ++j) {
-                        uint64_t &hh = h[c][j];
-                        hh = tc::f2_fma(e[t % 2][c][j], hh, tc::f2_mul(xx, o.b[j]));
-                        if (Y) acc = j ? tc::f2_fma(o.c[j], hh, acc) : tc::f2_mul(o.c[j], hh);
-                    }
-                    if (Y) part[c][t % 4] = tc::f2_lo(acc) + tc::f2_hi(acc);
-                    else sum_d[c] += o.dx[2 * c];
+                for (int j = 0; j < PR; ++j) {
+                    h[j] = tc::f2_fma(e[t % 2][j], h[j], tc::f2_mul(xx, o.b[j]));
+                    if (Y) acc = j ? tc::f2_fma(o.c[j], h[j], acc) : tc::f2_mul(o.c[j], h[j]);
                 }
-                if (Y && t % 4 == 3) {
-#pragma unroll
-                    for (int c = 0; c < CPT; ++c)
-                        *reinterpret_cast<float4 *>(&sm.y[ch + c][lane][t - 3]) =
-                            make_float4(part[c][0], part[c][1], part[c][2], part[c][3]);
+                if (Y) {
+                    part[t % 4] = tc::f2_lo(acc) + tc::f2_hi(acc);
+                    if (t % 4 == 3)
+                        *reinterpret_cast<float4 *>(&sm.y[ch][lane][t - 3]) = make_float4(part[0], part[1], part[2], part[3]);
+                } else {
+                    tile_d += o.dx.x;
                 }
             }
-        }
-        __syncwarp();
-        if (Y && inside && sc < nch) {
-            uint64_t y2[E / 2];
-#pragma unroll
-            for (int i = 0; i < E / 2; ++i)
-                y2[i] = tc::f2_fma(skip[i], tc::f2_make(to_f(ru.v[2 * i]), to_f(ru.v[2 * i + 1])),
-                                   tc::f2_make(sum_parts(sm.y[sc + 2 * i], sr), sum_parts(sm.y[sc + 2 * i + 1], sr)));
-            if (a.z) {
-                const Raw<T, E> rz = copied(k, 2, row_of(a.z, a.ldz, tr));
+            if (!Y) sum_d += tile_d;
+            __syncwarp();
+            if (Y && inside && sc < nch) {
+                uint64_t y2[E / 2];
 #pragma unroll
                 for (int i = 0; i < E / 2; ++i)
-                    y2[i] = tc::f2_mul(y2[i], tc::f2_make(swish(to_f(rz.v[2 * i])), swish(to_f(rz.v[2 * i + 1]))));
-            }
-            Raw<T, E> out;
+                    y2[i] = tc::f2_fma(skip[i], tc::f2_make(to_f(ru.v[2 * i]), to_f(ru.v[2 * i + 1])),
+                                       tc::f2_make(sum_parts(sm.y[sc + 2 * i], sr), sum_parts(sm.y[sc + 2 * i + 1], sr)));
+                if (a.z) {
+                    const Raw<T, E> rz = copied(k, 2, row_of(a.z, a.ldz, tr));
 #pragma unroll
-            for (int i = 0; i < E / 2; ++i) {
-                from_f(out.v[2 * i], tc::f2_lo(y2[i]));
-                from_f(out.v[2 * i + 1], tc::f2_hi(y2[i]));
+                    for (int i = 0; i < E / 2; ++i)
+                        y2[i] = tc::f2_mul(y2[i], tc::f2_make(swish(to_f(rz.v[2 * i])), swish(to_f(rz.v[2 * i + 1]))));
+                }
+                Raw<T, E> out;
+#pragma unroll
+                for (int i = 0; i < E / 2; ++i) {
+                    from_f(out.v[2 * i], tc::f2_lo(y2[i]));
+                    from_f(out.v[2 * i + 1], tc::f2_hi(y2[i]));
+                }
+                store_raw<T, E>(static_cast<T *>(a.y) + (row0 + tr) * a.D + c0 + sc, out, nch - sc);
             }
-            store_raw<T, E>(static_cast<T *>(a.y) + (row0 + tr) * a.D + c0 + sc, out, nch - sc);
         }
-      }
     };
 
     if (SPLIT) {
@@ -430,54 +411,188 @@ selective_scan_kernel(const ScanArgs a) {
         //    over all of them, exp(A sum d)
         if (me + 1 < segments) run(std::false_type{});
 #pragma unroll
-        for (int c = 0; c < CPT; ++c)
-#pragma unroll
-            for (int j = 0; j < PR; ++j) {
-                const uint64_t p = tc::f2_mul(dup(sum_d[c]), A2[c][j]);
-                const int n = state_of(2 * j);
-                // (a decay past the largest float would make NaN of a zero state)
-                *reinterpret_cast<float2 *>(&seg.a[ch + c][n]) = make_float2(fminf(exp2_fast(tc::f2_lo(p)), 3.4e38f), fminf(exp2_fast(tc::f2_hi(p)), 3.4e38f));
-                *reinterpret_cast<uint64_t *>(&seg.b[ch + c][n]) = h[c][j];
-            }
+        for (int j = 0; j < PR; ++j) {
+            const uint64_t p = tc::f2_mul(dup(sum_d), A2[j]);
+            const int n = state_of(2 * j);
+            // (a decay past the largest float would make NaN of a zero state)
+            *reinterpret_cast<float2 *>(&seg.a[ch][n]) =
+                make_float2(fminf(exp2_fast(tc::f2_lo(p)), 3.4e38f), fminf(exp2_fast(tc::f2_hi(p)), 3.4e38f));
+            *reinterpret_cast<uint64_t *>(&seg.b[ch][n]) = h[j];
+        }
         __syncthreads();
         if (first < end) copy_tile(first, 0, true);
         tc::cluster_sync();
         // 2. the state that enters this segment, through those before it
 #pragma unroll
-        for (int c = 0; c < CPT; ++c)
-#pragma unroll
-            for (int j = 0; j < PR; ++j) {
-                const uint32_t at_a = (uint32_t)__cvta_generic_to_shared(&seg.a[ch + c][state_of(2 * j)]);
-                const uint32_t at_b = (uint32_t)__cvta_generic_to_shared(&seg.b[ch + c][state_of(2 * j)]);
-                uint64_t e = 0;
-                if (me == 0 && a.s_in) {  // the entering state once more
-                    const int n = state_of(2 * j);
-                    const bool in = ch + c < nch;
-                    e = tc::f2_make(in && n < a.N ? a.s_in[state_row(c) + n] : 0.f,
-                                    in && n + 1 < a.N ? a.s_in[state_row(c) + n + 1] : 0.f);
-                }
-                for (int i = 0; i < me; ++i) {
-                    const float2 ai = tc::ld_cluster_f32x2(tc::map_to_rank(at_a, i));
-                    const float2 bi = tc::ld_cluster_f32x2(tc::map_to_rank(at_b, i));
-                    const uint64_t b2 = tc::f2_make(bi.x, bi.y);
-                    e = i ? tc::f2_fma(tc::f2_make(ai.x, ai.y), e, b2) : b2;
-                }
-                h[c][j] = e;
+        for (int j = 0; j < PR; ++j) {
+            const uint32_t at_a = (uint32_t)__cvta_generic_to_shared(&seg.a[ch][state_of(2 * j)]);
+            const uint32_t at_b = (uint32_t)__cvta_generic_to_shared(&seg.b[ch][state_of(2 * j)]);
+            h[j] = me == 0 ? entering(j) : 0;
+            for (int i = 0; i < me; ++i) {
+                const float2 ai = tc::ld_cluster_f32x2(tc::map_to_rank(at_a, i));
+                const float2 bi = tc::ld_cluster_f32x2(tc::map_to_rank(at_b, i));
+                const uint64_t b2 = tc::f2_make(bi.x, bi.y);
+                h[j] = i ? tc::f2_fma(tc::f2_make(ai.x, ai.y), h[j], b2) : b2;
             }
+        }
         tc::cluster_sync();  // nothing of this CTA's is read after this; state_out may be state_in
     }
     run(std::true_type{});
     if (SPLIT && me + 1 < segments) return;
-    if (a.s_out) {
+    if (a.s_out && ch < nch) {
 #pragma unroll
-        for (int c = 0; c < CPT; ++c)
-#pragma unroll
-            for (int j = 0; j < PR; ++j) {
-                const int n = state_of(2 * j);  // n + 1 is the pair's other state
-                if (ch + c < nch && n < a.N) a.s_out[state_row(c) + n] = tc::f2_lo(h[c][j]);
-                if (ch + c < nch && n + 1 < a.N) a.s_out[state_row(c) + n + 1] = tc::f2_hi(h[c][j]);
-            }
+        for (int j = 0; j < PR; ++j) {
+            const int n = state_of(2 * j);  // n + 1 is the pair's other state
+            if (n < a.N) a.s_out[state_row + n] = tc::f2_lo(h[j]);
+            if (n + 1 < a.N) a.s_out[state_row + n + 1] = tc::f2_hi(h[j]);
+        }
     }
+}
+
+// A few rows per sequence (single tokens): bound by the state, which is read and
+// written once.  A thread holds V times four states of a channel; `lanes` threads
+// (a power of two, two where N allows, so that a read covers whole 32-byte
+// sectors) share the channel, and u, d and the step's softplus are worked out once
+// per thread.  Several sequences per thread (A read once for them) measured
+// slower, since the registers cost resident warps: 64 x 4096 x 16 states 13.0 us
+// with four, 10.6 with one.  ONE: L = 1 (9.2 -> 8.6 us for the same).
+constexpr int kTokenRows = 8;  // longest L
+constexpr int kTokenThreads = 128;
+
+template <typename T, int V, bool VEC, bool ONE>
+__global__ void __launch_bounds__(kTokenThreads)
+selective_token_kernel(const ScanArgs a, int lanes) {
+    const int idx = blockIdx.x * kTokenThreads + threadIdx.x;
+    const int c = idx / lanes, lane = idx % lanes;
+    const int b = blockIdx.y;
+    const bool live = c < a.D;
+    const int cc = live ? c : a.D - 1;  // the other threads of the warp take part in its shuffles
+    const int g = cc / a.dpg;
+    auto first = [&](int v) { return 4 * (lane + lanes * v); };  // state of piece v
+    auto states = [&](int v) { return live ? min(4, a.N - first(v)) : 0; };
+    float A2[V][4];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
+        const float *p = a.A + (long long)cc * a.N + first(v);
+        if (VEC) {
+            if (states(v) > 0) r = *reinterpret_cast<const float4 *>(p);
+        } else {
+            if (states(v) > 0) r.x = p[0];
+            if (states(v) > 1) r.y = p[1];
+            if (states(v) > 2) r.z = p[2];
+            if (states(v) > 3) r.w = p[3];
+        }
+        A2[v][0] = r.x * kLog2e; A2[v][1] = r.y * kLog2e; A2[v][2] = r.z * kLog2e; A2[v][3] = r.w * kLog2e;
+    }
+    const float bias = a.bias ? a.bias[cc] : 0.f, skip = a.skip ? a.skip[cc] : 0.f;
+    float h[V][4];
+    const int len = a.lengths ? min(max(a.lengths[b], 0), a.L) : a.L;
+    const long long state_row = ((long long)b * a.D + cc) * a.N;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const float *p = a.s_in + state_row + first(v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h[v][i] = 0.f;
+        if (a.s_in && states(v) > 0) {
+            if (VEC) {
+                *reinterpret_cast<float4 *>(h[v]) = __ldcs(reinterpret_cast<const float4 *>(p));
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (i < states(v)) h[v][i] = p[i];
+            }
+        }
+    }
+    for (int t = 0; t < (ONE ? 1 : a.L); ++t) {
+        const bool in = t < len;
+        const long long row = (long long)b * a.L + t;
+        const float u = in ? to_f(static_cast<const T *>(a.u)[row * a.ldu + cc]) : 0.f;
+        float d = in ? to_f(static_cast<const T *>(a.delta)[row * a.ldd + cc]) : 0.f;
+        const float z = in && a.z ? to_f(static_cast<const T *>(a.z)[row * a.ldz + cc]) : 0.f;
+        const T *pb = static_cast<const T *>(a.bm) + row * a.ldb + (long long)g * a.N;
+        const T *pc = static_cast<const T *>(a.cm) + row * a.ldc + (long long)g * a.N;
+        Raw<T, 4> rb[V], rc[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                from_f(rb[v].v[i], 0.f);
+                from_f(rc[v].v[i], 0.f);
+            }
+            if (VEC) {
+                if (in && states(v) > 0) {
+                    rb[v] = *reinterpret_cast<const Raw<T, 4> *>(pb + first(v));
+                    rc[v] = *reinterpret_cast<const Raw<T, 4> *>(pc + first(v));
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (in && i < states(v)) {
+                        rb[v].v[i] = pb[first(v) + i];
+                        rc[v].v[i] = pc[first(v) + i];
+                    }
+            }
+        }
+        d += bias;
+        if (a.softplus) d = tc::f2_lo(softplus2(dup(d)));
+        if (!in) d = 0.f;
+        const float x = d * u;
+        float y = 0.f;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                h[v][i] = fmaf(exp2_fast(d * A2[v][i]), h[v][i], x * to_f(rb[v].v[i]));
+                y = fmaf(to_f(rc[v].v[i]), h[v][i], y);
+            }
+        for (int m = lanes / 2; m > 0; m >>= 1) y += __shfl_xor_sync(0xffffffffu, y, m);
+        if (lane == 0 && live && in) {
+            y = fmaf(skip, u, y);
+            if (a.z) y *= swish(z);
+            from_f(static_cast<T *>(a.y)[row * a.D + c], y);
+        }
+    }
+    if (!a.s_out) return;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        float *p = a.s_out + state_row + first(v);
+        if (states(v) <= 0) continue;
+        if (VEC) {
+            __stcs(reinterpret_cast<float4 *>(p), *reinterpret_cast<float4 *>(h[v]));
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i < states(v)) p[i] = h[v][i];
+        }
+    }
+}
+
+template <typename T, int V>
+cudaError_t launch_token_t(const ScanArgs &a, int lanes, cudaStream_t st) {
+    const long long bx = ((long long)a.D * lanes + kTokenThreads - 1) / kTokenThreads;
+    if ((long long)a.D * lanes > 0x7fffff00LL || a.B > 65535) return cudaErrorInvalidConfiguration;
+    // whole float4s of states, and 4-element pieces of B and C on their size
+    auto fits = [](const void *p, long long ld) {
+        return (reinterpret_cast<uintptr_t>(p) & (4 * sizeof(T) - 1)) == 0 && ld % 4 == 0;
+    };
+    const bool vec = a.N % 4 == 0 && fits(a.bm, a.ldb) && fits(a.cm, a.ldc), one = a.L == 1;
+    auto kern = vec ? one ? selective_token_kernel<T, V, true, true> : selective_token_kernel<T, V, true, false>
+                    : one ? selective_token_kernel<T, V, false, true> : selective_token_kernel<T, V, false, false>;
+    kern<<<dim3((unsigned)bx, (unsigned)a.B), kTokenThreads, 0, st>>>(a, lanes);
+    const cudaError_t err = cudaGetLastError();
+    if (err == cudaSuccess) note_launches(1);
+    return err;
+}
+
+template <typename T>
+cudaError_t launch_tokens(const ScanArgs &a, cudaStream_t st) {
+    if (a.N <= 4) return launch_token_t<T, 1>(a, 1, st);
+    if (a.N <= 8) return launch_token_t<T, 1>(a, 2, st);
+    if (a.N <= 16) return launch_token_t<T, 2>(a, 2, st);
+    if (a.N <= 32) return launch_token_t<T, 2>(a, 4, st);
+    if (a.N <= 64) return launch_token_t<T, 4>(a, 4, st);
+    return launch_token_t<T, 4>(a, 8, st);
 }
 
 // Segments a sequence is cut into.  One warp per scheduler alone takes about 170
@@ -490,23 +605,27 @@ int segments_of(long long warps, int L, int tile) {
         return (s > 1 ? 1.8 : 1.0) / s * (90.0 + 81.0 * w);
     };
     int best = 1;
-    for (int s = 4; s <= 8; s *= 2)
+    for (int s = 4; s <= 16; s *= 2)
         if (L >= s * 4 * tile && cost(s) < cost(best)) best = s;
     return best;
 }
 
-template <typename T, int SPT, int LANES_, int CPT, bool VEC>
+template <typename T, int SPT, int LANES, bool VEC>
 cudaError_t launch_vec(ScanArgs a, cudaStream_t st) {
-    using C = ScanTile<T, SPT, LANES_, CPT, VEC>;
+    using C = ScanTile<T, SPT, LANES, VEC>;
     a.blocks_per_group = (a.dpg + C::CH - 1) / C::CH;
     const long long blocks = (long long)a.B * a.G * a.blocks_per_group;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     const int segments = segments_of(blocks * C::WARPS, a.L, C::TT);
-    auto kern = segments > 1 ? selective_scan_kernel<T, SPT, LANES_, CPT, VEC, true>
-                             : selective_scan_kernel<T, SPT, LANES_, CPT, VEC, false>;
+    auto kern = segments > 1 ? selective_scan_kernel<T, SPT, LANES, VEC, true>
+                             : selective_scan_kernel<T, SPT, LANES, VEC, false>;
     const size_t smem = sizeof(typename C::Smem) + (segments > 1 ? sizeof(typename C::Segment) : 0);
     cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (err != cudaSuccess) return err;
+    if (segments > 8) {
+        err = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (err != cudaSuccess) return err;
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)blocks, (unsigned)segments);
     cfg.blockDim = dim3(C::NT);
@@ -524,23 +643,24 @@ cudaError_t launch_vec(ScanArgs a, cudaStream_t st) {
     return err;
 }
 
-template <typename T, int SPT, int LANES_, int CPT>
+template <typename T, int SPT, int LANES>
 cudaError_t launch_scan(const ScanArgs &a, cudaStream_t st) {
     auto fits = [](const void *p, long long ld) {
         return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld * (long long)sizeof(T) % 16 == 0;
     };
     const bool vec = fits(a.u, a.ldu) && fits(a.delta, a.ldd) && (!a.z || fits(a.z, a.ldz)) && fits(a.bm, a.ldb) &&
                      fits(a.cm, a.ldc) && fits(a.y, a.D) && (a.G == 1 || (fits(nullptr, a.dpg) && fits(nullptr, a.N)));
-    return vec ? launch_vec<T, SPT, LANES_, CPT, true>(a, st) : launch_vec<T, SPT, LANES_, CPT, false>(a, st);
+    return vec ? launch_vec<T, SPT, LANES, true>(a, st) : launch_vec<T, SPT, LANES, false>(a, st);
 }
 
 template <typename T>
 cudaError_t launch_n(const ScanArgs &a, cudaStream_t st) {
-    if (a.N <= 8) return launch_scan<T, 4, 2, 1>(a, st);
-    if (a.N <= 16) return launch_scan<T, 8, 2, 1>(a, st);
-    if (a.N <= 32) return launch_scan<T, 8, 4, 1>(a, st);
-    if (a.N <= 64) return launch_scan<T, 8, 8, 1>(a, st);
-    return launch_scan<T, 16, 8, 1>(a, st);
+    if (a.L <= kTokenRows && a.B <= 65535) return launch_tokens<T>(a, st);
+    if (a.N <= 8) return launch_scan<T, 4, 2>(a, st);
+    if (a.N <= 16) return launch_scan<T, 8, 2>(a, st);
+    if (a.N <= 32) return launch_scan<T, 8, 4>(a, st);
+    if (a.N <= 64) return launch_scan<T, 8, 8>(a, st);
+    return launch_scan<T, 16, 8>(a, st);
 }
 
 bool aligned(const void *p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
