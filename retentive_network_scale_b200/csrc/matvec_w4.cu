@@ -26,7 +26,11 @@
 namespace ret {
 namespace {
 
-constexpr int kWarps = 8, kThreads = 32 * kWarps;
+
+// Threads of a CTA: sixteen warps where the accumulators leave them registers.
+__host__ __device__ constexpr int max_threads(int NT) { return NT <= 2 ? 512 : 256; }
+constexpr size_t kStage = 64 * 1024;  // bytes of x staged at a time
+constexpr int kSms = 148;
 
 struct W4Args {
     int M, N, K, x_dtype, xg, cols;  // xg: columns of x per x scale; cols: columns of the products
@@ -36,16 +40,20 @@ struct W4Args {
     const uint8_t *wq, *zeros;
     const __nv_bfloat16 *s;
     void *y;
-    int y_bf16, kc;  // kc: columns of x staged at a time
+    int y_bf16, vec;
+    int kc;                 // columns of x staged at a time
+    int wr, wk, tile_cols;  // row tiles of a CTA, warps to a tile, product columns of a CTA
+    int xgrouped;           // x scales by group of columns, not by row
 };
 
+// c = a b + (FIRST ? 0 : c)
+template <bool FIRST>
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    const float c0 = FIRST ? 0.f : c[0], c1 = FIRST ? 0.f : c[1], c2 = FIRST ? 0.f : c[2], c3 = FIRST ? 0.f : c[3];
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
-
 // Codes (k+j, k+j+4) of the 8 codes in w, as bf16 minus `zero` (both lanes of
 // it 128 + z): exact.
 template <int J>
@@ -77,141 +85,250 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// 8 columns of x from column k of product column `col`, as bf16 pairs (j, j+4).
-__device__ __forceinline__ uint4 load_x(const W4Args &a, int col, int k) {
-    float v[8];
-    if (a.x_dtype == RET_F32) {
-        const int m = col / 3, part = col - 3 * m;
-        const float *p = static_cast<const float *>(a.x) + (long long)m * a.ldx + k;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            // parts of 8 bits each: what the parts before it leave
-            const float x = p[i];
-            float r = x;
-            for (int j = 0; j < part; ++j) {
-                const float top = __bfloat162float(__float2bfloat16_rn(r));
-                r = isfinite(top) ? r - top : 0.f;  // infinities and NaN go with the first part
-            }
-            v[i] = r;
-        }
-    } else if (a.x_dtype == RET_BF16) {
-        const __nv_bfloat16 *p = static_cast<const __nv_bfloat16 *>(a.x) + (long long)col * a.ldx + k;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = __bfloat162float(p[i]);
-    } else {
-        const uint8_t *p = static_cast<const uint8_t *>(a.x) + (long long)col * a.ldx + k;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            v[i] = a.x_dtype == RET_I8 ? (float)(int8_t)p[i]
-                                       : __half2float(__half(__nv_cvt_fp8_to_halfraw(p[i], __NV_E4M3)));
-    }
+// bf16 pairs (j, j + 4) of 8 values.
+__device__ __forceinline__ uint4 pack_x(const float (&v)[8]) {
     return make_uint4(pack_bf16(v[0], v[4]), pack_bf16(v[1], v[5]), pack_bf16(v[2], v[6]), pack_bf16(v[3], v[7]));
 }
+// 8 columns of an x row as loaded (16 bytes of bf16, 8 of codes, 32 of fp32).
+struct RawX {
+    uint4 q[2];
+};
+// a.vec: rows of x start on the size of 8 elements (16 bytes for fp32).
+__device__ __forceinline__ void load_x(const W4Args &a, RawX &r, int m, int k) {
+    if (a.x_dtype == RET_BF16) {
+        const uint16_t *p = static_cast<const uint16_t *>(a.x) + (long long)m * a.ldx + k;
+        r.q[0] = a.vec ? *reinterpret_cast<const uint4 *>(p)
+                       : make_uint4(p[0] | (uint32_t)p[1] << 16, p[2] | (uint32_t)p[3] << 16, p[4] | (uint32_t)p[5] << 16,
+                                    p[6] | (uint32_t)p[7] << 16);
+    } else if (a.x_dtype == RET_F32) {
+        const uint32_t *p = static_cast<const uint32_t *>(a.x) + (long long)m * a.ldx + k;
+        r.q[0] = a.vec ? *reinterpret_cast<const uint4 *>(p) : make_uint4(p[0], p[1], p[2], p[3]);
+        r.q[1] = a.vec ? *reinterpret_cast<const uint4 *>(p + 4) : make_uint4(p[4], p[5], p[6], p[7]);
+    } else {
+        const uint8_t *p = static_cast<const uint8_t *>(a.x) + (long long)m * a.ldx + k;
+        const uint2 u = a.vec ? *reinterpret_cast<const uint2 *>(p)
+                              : make_uint2(p[0] | (uint32_t)p[1] << 8 | (uint32_t)p[2] << 16 | (uint32_t)p[3] << 24,
+                                           p[4] | (uint32_t)p[5] << 8 | (uint32_t)p[6] << 16 | (uint32_t)p[7] << 24);
+        r.q[0].x = u.x;
+        r.q[0].y = u.y;
+    }
+}
+// Them as bf16 pairs (j, j + 4): for fp32 rows the three parts of 8 bits each,
+// dst[0], dst[4] and dst[8].
+__device__ __forceinline__ void stage_x(const W4Args &a, const RawX &r, uint4 *dst) {
+    const uint4 u = r.q[0], t = r.q[1];
+    if (a.x_dtype == RET_BF16) {
+        *dst = make_uint4(__byte_perm(u.x, u.z, 0x5410), __byte_perm(u.x, u.z, 0x7632), __byte_perm(u.y, u.w, 0x5410),
+                          __byte_perm(u.y, u.w, 0x7632));
+    } else if (a.x_dtype == RET_F32) {
+        const uint32_t bits[8] = {u.x, u.y, u.z, u.w, t.x, t.y, t.z, t.w};
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(bits[i]);
+#pragma unroll
+        for (int j = 0; j < 3; ++j) {
+            const uint4 p = pack_x(v);
+            dst[4 * j] = p;
+            const uint32_t w[4] = {p.x, p.y, p.z, p.w};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {  // what this part leaves
+                const float top = __uint_as_float(i < 4 ? w[i] << 16 : w[i - 4] & 0xffff0000u);
+                v[i] = fabsf(top) <= 3.4e38f ? v[i] - top : 0.f;  // infinities and NaN go with the first part
+            }
+        }
+    } else {
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t w = i < 4 ? u.x : u.y;
+            if (a.x_dtype == RET_I8)  // 2^23 + 128 + code, minus 2^23 + 128
+                v[i] = __uint_as_float(__byte_perm(w ^ 0x80808080u, 0x4b000000u, 0x7650 + i % 4)) - 8388736.f;
+            else
+                v[i] = __half2float(__half(__nv_cvt_fp8_to_halfraw((uint8_t)(w >> (8 * (i % 4))), __NV_E4M3)));
+        }
+        *dst = pack_x(v);
+    }
+}
 
-// One CTA: 16 weight rows, all K; its warps take the groups of the rows in
-// turn and their sums meet in shared memory.  WPL: 32-bit words of codes per
-// load, a group of weights being 32 WPL columns: the four lanes of a row read
-// one group in one load each.  NT: 8-column tiles of x.
-template <int WPL, int NT>
-__global__ void __launch_bounds__(kThreads)
+// One CTA: `wr` tiles of 16 weight rows, `wk` warps to a tile that share its groups,
+// their sums meeting in shared memory.  x is staged kc columns at a time; of a
+// chunk's groups each of the wk warps takes a stretch.  WPL: 32-bit words of codes
+// per load, a group of weights being 32 WPL columns: the four lanes of a row read
+// one group in one load each.  NT: 8-column tiles of x.  PF: groups requested ahead,
+// across chunks.  ZP: with zero points.  XG: x scales by group of columns.
+template <int WPL, int NT, int PF, bool ZP, bool XG>
+__global__ void __launch_bounds__(max_threads(NT))
 matvec_w4_kernel(const W4Args a) {
     constexpr int GK = 32 * WPL;
     extern __shared__ __align__(16) uint8_t dsm[];
-    uint4 *xs = reinterpret_cast<uint4 *>(dsm);  // [kc / 32][cols][4]
+    uint4 *xs = reinterpret_cast<uint4 *>(dsm);  // [kc / 32][columns][4]
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, q = lane / 4, c = lane % 4;
-    const int n0 = blockIdx.x * 16;
-    const int col0 = blockIdx.y * NT * 8, ncol = min(NT * 8, a.cols - col0);
+    const int wr = a.wr, wk = a.wk, mr = warp % wr, mk = warp / wr;
+    const int n0 = (blockIdx.x * wr + mr) * 16;
+    const int per = a.x_dtype == RET_F32 ? 3 : 1;  // product columns of an x row
+    const int col0 = blockIdx.y * a.tile_cols, ncol = min(a.tile_cols, a.cols - col0), nrow = ncol / per;
     const int groups = a.K / GK;
+    // groups of a chunk, and of it of this warp
+    const int gc = a.kc / GK, stretch = (gc + wk - 1) / wk, lo = min(mk * stretch, gc), hi = min(lo + stretch, gc);
+
+    struct Weights {
+        uint32_t w[2][WPL];
+        uint16_t s[2];
+        uint8_t z[2];
+    };
+    // rows q and q + 8 of the tile (rows past the last repeat it)
     const int r0 = min(n0 + q, a.N - 1), r1 = min(n0 + q + 8, a.N - 1);
-    const uint8_t *w0 = a.wq + (long long)r0 * (a.K / 2), *w1 = a.wq + (long long)r1 * (a.K / 2);
-    const long long s0 = (long long)r0 * groups, s1 = (long long)r1 * groups;
+    const uint8_t *w0 = a.wq + (long long)r0 * (a.K / 2) + c * 4 * WPL, *w1 = a.wq + (long long)r1 * (a.K / 2) + c * 4 * WPL;
+    const unsigned short *s0 = reinterpret_cast<const unsigned short *>(a.s) + (long long)r0 * groups;
+    const unsigned short *s1 = reinterpret_cast<const unsigned short *>(a.s) + (long long)r1 * groups;
+    const uint8_t *z0 = a.zeros + (ZP ? (long long)r0 * groups : 0), *z1 = a.zeros + (ZP ? (long long)r1 * groups : 0);
+    int ahead = lo, ahead_hi = min(hi, groups);  // next group to request; end of the stretch it is of
+    auto fetch = [&](Weights &o) {
+        if (ahead >= ahead_hi) {  // on to this warp's stretch of the next chunk
+            ahead += gc - (hi - lo);
+            ahead_hi = min(ahead_hi + gc, groups);
+            if (lo >= hi) return;
+        }
+        if (ahead < ahead_hi) {
+            load_words<WPL>(o.w[0], w0 + (unsigned)ahead * (GK / 2));
+            load_words<WPL>(o.w[1], w1 + (unsigned)ahead * (GK / 2));
+            o.s[0] = __ldg(s0 + ahead);
+            o.s[1] = __ldg(s1 + ahead);
+            if (ZP) {
+                o.z[0] = __ldg(z0 + ahead);
+                o.z[1] = __ldg(z1 + ahead);
+            }
+        }
+        ++ahead;
+    };
+    Weights ring[PF];
+#pragma unroll
+    for (int i = 0; i < PF; ++i) fetch(ring[i]);
 
     float acc[NT][4];
+    int xat[NT];  // this lane's place in a step's columns (columns past the last repeat it)
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
+    for (int i = 0; i < NT; ++i) {
+        xat[i] = min(8 * i + q, ncol - 1) * 4 + c;
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+    }
 
+    // staging: this thread's first piece of a chunk, and the way to its next ones
+    const int row_first = tid / 4 % nrow, step_first = tid / 4 / nrow;
+    const int row_next = (int)blockDim.x / 4 % nrow, step_next = (int)blockDim.x / 4 / nrow;
     for (int k0 = 0; k0 < a.K; k0 += a.kc) {
         const int kn = min(a.kc, a.K - k0);
         if (k0) __syncthreads();
         // x of the chunk: piece (step of 32 columns, product column, c) holds
         // the 8 columns that lane c multiplies in that step
-        for (int i = tid; i < kn / 8 * ncol; i += kThreads) {
-            const int cc = i % 4, col = i / 4 % ncol, step = i / (4 * ncol);
-            const int blk = step / WPL, j = step % WPL;
-            xs[i] = load_x(a, col0 + col, k0 + blk * GK + cc * 8 * WPL + 8 * j);
+        constexpr int UX = 2;  // pieces a thread has in flight
+        int row = row_first, st = step_first;
+        while (st < kn / 32) {
+            RawX raw[UX];
+            int at[UX];
+#pragma unroll
+            for (int u = 0; u < UX; ++u) {
+                at[u] = st < kn / 32 ? (st * ncol + row * per) * 4 + tid % 4 : -1;
+                if (at[u] >= 0) load_x(a, raw[u], col0 / per + row, k0 + st / WPL * GK + tid % 4 * 8 * WPL + 8 * (st % WPL));
+                row += row_next;
+                st += step_next;
+                if (row >= nrow) {
+                    row -= nrow;
+                    ++st;
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < UX; ++u)
+                if (at[u] >= 0) stage_x(a, raw[u], xs + at[u]);
         }
         __syncthreads();
-        for (int blk = warp; blk < kn / GK; blk += kWarps) {
-            const int gi = k0 / GK + blk;
-            uint32_t wa[WPL], wb[WPL];
-            load_words<WPL>(wa, w0 + (long long)gi * (GK / 2) + c * 4 * WPL);
-            load_words<WPL>(wb, w1 + (long long)gi * (GK / 2) + c * 4 * WPL);
-            const float sa = __bfloat162float(a.s[s0 + gi]), sb = __bfloat162float(a.s[s1 + gi]);
-            const uint32_t za = a.zeros ? 0x4300u + (a.zeros[s0 + gi] & 15u) : 0x4308u;
-            const uint32_t zb = a.zeros ? 0x4300u + (a.zeros[s1 + gi] & 15u) : 0x4308u;
-            const uint32_t za2 = za | za << 16, zb2 = zb | zb << 16;
-            const __nv_bfloat162 zeroa = *reinterpret_cast<const __nv_bfloat162 *>(&za2);
-            const __nv_bfloat162 zerob = *reinterpret_cast<const __nv_bfloat162 *>(&zb2);
+        const int g1 = min(hi, kn / GK);
+        const uint4 *xp = xs + lo * (WPL * 4) * ncol;
+        auto group = [&](Weights &o, int g) {
             float sum[NT][4];
-#pragma unroll
-            for (int i = 0; i < NT; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) sum[i][j] = 0.f;
+            float more[4];  // one column tile: a second chain of products
+            const uint32_t za = ZP ? 0x43004300u + (o.z[0] & 15u) * 0x10001u : 0x43084308u;
+            const uint32_t zb = ZP ? 0x43004300u + (o.z[1] & 15u) * 0x10001u : 0x43084308u;
+            const __nv_bfloat162 zero0 = *reinterpret_cast<const __nv_bfloat162 *>(&za);
+            const __nv_bfloat162 zero1 = *reinterpret_cast<const __nv_bfloat162 *>(&zb);
 #pragma unroll
             for (int j = 0; j < WPL; ++j) {
-                const uint32_t fa[4] = {code_pair<0>(wa[j], zeroa), code_pair<0>(wb[j], zerob),
-                                        code_pair<1>(wa[j], zeroa), code_pair<1>(wb[j], zerob)};
-                const uint32_t fb[4] = {code_pair<2>(wa[j], zeroa), code_pair<2>(wb[j], zerob),
-                                        code_pair<3>(wa[j], zeroa), code_pair<3>(wb[j], zerob)};
+                uint4 b[NT];
+#pragma unroll
+                for (int i = 0; i < NT; ++i) b[i] = xp[xat[i]];
+                xp += 4 * ncol;
+                const uint32_t wa = o.w[0][j], wb = o.w[1][j];
+                const uint32_t fa[4] = {code_pair<0>(wa, zero0), code_pair<0>(wb, zero1), code_pair<1>(wa, zero0),
+                                        code_pair<1>(wb, zero1)};
+                const uint32_t fb[4] = {code_pair<2>(wa, zero0), code_pair<2>(wb, zero1), code_pair<3>(wa, zero0),
+                                        code_pair<3>(wb, zero1)};
 #pragma unroll
                 for (int i = 0; i < NT; ++i) {
-                    const int col = 8 * i + q;
-                    uint4 b = make_uint4(0, 0, 0, 0);
-                    if (col < ncol) b = xs[((blk * WPL + j) * ncol + col) * 4 + c];
-                    mma16816(sum[i], fa, b.x, b.y);
-                    mma16816(sum[i], fb, b.z, b.w);
+                    if (j == 0) mma16816<true>(sum[i], fa, b[i].x, b[i].y);
+                    else mma16816<false>(sum[i], fa, b[i].x, b[i].y);
+                    if (NT > 1) mma16816<false>(sum[i], fb, b[i].z, b[i].w);
+                    else if (j == 0) mma16816<true>(more, fb, b[i].z, b[i].w);
+                    else mma16816<false>(more, fb, b[i].z, b[i].w);
                 }
             }
-            const int per = a.x_dtype == RET_F32 ? 3 : 1;
+            if (NT == 1)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) sum[0][j] += more[j];
+            const float sa = __uint_as_float((uint32_t)o.s[0] << 16), sb = __uint_as_float((uint32_t)o.s[1] << 16);
+            if (XG) {
+                const int xgs = a.K / a.xg, xi = (k0 + g * GK) / a.xg;
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
+                    const int m0 = min(col0 + 8 * i + 2 * c, a.cols - 1), m1 = min(col0 + 8 * i + 2 * c + 1, a.cols - 1);
+                    const float x0 = a.xs[(long long)m0 * xgs + xi], x1 = a.xs[(long long)m1 * xgs + xi];
+                    sum[i][0] *= x0;
+                    sum[i][1] *= x1;
+                    sum[i][2] *= x0;
+                    sum[i][3] *= x1;
+                }
+            }
 #pragma unroll
             for (int i = 0; i < NT; ++i) {
-                float x0 = 1.f, x1 = 1.f;
-                if (a.xs && a.xg < a.K) {  // x scales by group of columns
-                    const int m0 = col0 + 8 * i + 2 * c, xgs = a.K / a.xg, xi = gi * GK / a.xg;
-                    if (m0 < a.cols) x0 = a.xs[(long long)(m0 / per) * xgs + xi];
-                    if (m0 + 1 < a.cols) x1 = a.xs[(long long)((m0 + 1) / per) * xgs + xi];
-                }
-                acc[i][0] = fmaf(sa * x0, sum[i][0], acc[i][0]);
-                acc[i][1] = fmaf(sa * x1, sum[i][1], acc[i][1]);
-                acc[i][2] = fmaf(sb * x0, sum[i][2], acc[i][2]);
-                acc[i][3] = fmaf(sb * x1, sum[i][3], acc[i][3]);
+                acc[i][0] = fmaf(sa, sum[i][0], acc[i][0]);
+                acc[i][1] = fmaf(sa, sum[i][1], acc[i][1]);
+                acc[i][2] = fmaf(sb, sum[i][2], acc[i][2]);
+                acc[i][3] = fmaf(sb, sum[i][3], acc[i][3]);
             }
-        }
+            fetch(o);
+        };
+        int g = lo;
+#pragma unroll 1
+        for (; g + PF <= g1; g += PF)
+#pragma unroll
+            for (int p = 0; p < PF; ++p) group(ring[p], g + p);
+        // the rest of a stretch (the last one's: whole chunks hold whole rings)
+#pragma unroll
+        for (int p = 0; p < PF - 1; ++p)
+            if (g + p < g1) group(ring[p], g + p);
     }
-    // join the warps' sums: red[warp][16 rows][NT*8 columns + 1]
+    // join the warps' sums: red[mk][rows of the CTA][NT*8 columns + 1]
     __syncthreads();
     float *red = reinterpret_cast<float *>(dsm);
     constexpr int RS = NT * 8 + 1;
+    const int rows = wr * 16;
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-        float *p = red + (warp * 16 + q) * RS + 8 * i + 2 * c;
+        float *p = red + (mk * rows + mr * 16 + q) * RS + 8 * i + 2 * c;
         p[0] = acc[i][0];
         p[1] = acc[i][1];
         p[8 * RS] = acc[i][2];
         p[8 * RS + 1] = acc[i][3];
     }
     __syncthreads();
-    const int per = a.x_dtype == RET_F32 ? 3 : 1;
-    for (int i = tid; i < 16 * (ncol / per); i += kThreads) {
-        const int r = i % 16, m = i / 16, n = n0 + r;
+    for (int i = tid; i < rows * nrow; i += blockDim.x) {
+        const int r = i % rows, m = i / rows, n = blockIdx.x * rows + r;
         if (n >= a.N) continue;
         float y = 0.f;
         for (int p = per - 1; p >= 0; --p)
-            for (int w = 0; w < kWarps; ++w) y += red[(w * 16 + r) * RS + m * per + p];
+            for (int w = 0; w < wk; ++w) y += red[(w * rows + r) * RS + m * per + p];
         const int mm = col0 / per + m;
-        if (a.xs && a.xg == a.K) y *= a.xs[mm];
+        if (a.xs && !a.xgrouped) y *= a.xs[mm];
         const long long at = (long long)mm * a.N + n;
         if (a.y_bf16)
             static_cast<__nv_bfloat16 *>(a.y)[at] = __float2bfloat16_rn(y);
@@ -222,16 +339,41 @@ matvec_w4_kernel(const W4Args a) {
 
 template <int WPL, int NT>
 cudaError_t launch_w4(W4Args a, cudaStream_t st) {
-    constexpr int RS = NT * 8 + 1;
-    const int ncol = std::min(a.cols, NT * 8);
-    const int limit = 96 * 1024 / (2 * ncol) / 128 * 128;
-    a.kc = std::min((a.K + 127) / 128 * 128, std::max(limit, 128));
-    const size_t smem = std::max((size_t)a.kc * 2 * ncol, sizeof(float) * kWarps * 16 * RS);
-    const long long bx = ((long long)a.N + 15) / 16, by = (a.cols + NT * 8 - 1) / (NT * 8);
-    auto kern = matvec_w4_kernel<WPL, NT>;
+    constexpr int PF = WPL == 4 ? 4 : 8;  // 16 words a row ahead (8 of the smallest groups)
+    const int per = a.x_dtype == RET_F32 ? 3 : 1;
+    a.tile_cols = std::min(a.cols, NT * 8 / per * per);  // whole rows of x
+    const int groups = a.K / (32 * WPL);
+    const long long tiles = ((long long)a.N + 15) / 16;
+    const size_t x_bytes = (size_t)a.K * 2 * a.tile_cols;
+    auto unit = [&](int wk) { return 32 * WPL * PF * wk; };  // columns: one ring of each warp
+    // The CTA that leaves the fullest SM least to do, counted in instructions (a
+    // group's, x's staging and a CTA's own), each tile of rows shared by as many
+    // warps as fit, down to two groups each.  One token times 2048 x 12288: 6.9 us
+    // with 6 tiles of 2 warps (128 CTAs), 8.2 with 2 of 4, 10.5 with 1 of 8.
+    const int most = max_threads(NT) / 32;
+    double best = 1e300;
+    for (int wr = most; wr >= 1; --wr) {
+        int wk = std::max(1, std::min(most / wr, groups / 2));
+        while (wk > 1 && x_bytes > kStage && (size_t)unit(wk) * 2 * a.tile_cols > 2 * kStage) --wk;
+        const double ctas = (double)(((tiles + wr - 1) / wr + kSms - 1) / kSms);
+        const double group = (wr * wk) * (double)((groups + wk - 1) / wk) * (WPL * (30 + 4 * NT) + 60 + 8 * NT);
+        const double cost = ctas * (group + (double)a.K * a.tile_cols / 256 * 20 + 3000);
+        if (cost < best) {
+            best = cost;
+            a.wr = wr;
+            a.wk = wk;
+        }
+    }
+    // a chunk holds whole rings of every warp, or all of x
+    a.kc = x_bytes <= kStage ? a.K : std::max(1, (int)(kStage / (2 * a.tile_cols) / unit(a.wk))) * unit(a.wk);
+    if (a.kc > a.K) a.kc = a.K;
+    const size_t smem = std::max((size_t)a.kc * 2 * a.tile_cols, sizeof(float) * a.wk * a.wr * 16 * (NT * 8 + 1));
+    const long long bx = (tiles + a.wr - 1) / a.wr, by = (a.cols + a.tile_cols - 1) / a.tile_cols;
+    auto kern = a.zeros ? a.xgrouped ? matvec_w4_kernel<WPL, NT, PF, true, true> : matvec_w4_kernel<WPL, NT, PF, true, false>
+                        : a.xgrouped ? matvec_w4_kernel<WPL, NT, PF, false, true> : matvec_w4_kernel<WPL, NT, PF, false, false>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    kern<<<dim3((unsigned)bx, (unsigned)by), kThreads, smem, st>>>(a);
+    kern<<<dim3((unsigned)bx, (unsigned)by), 32 * a.wr * a.wk, smem, st>>>(a);
     e = cudaGetLastError();
     if (e == cudaSuccess) note_launches(1);
     return e;
@@ -239,11 +381,10 @@ cudaError_t launch_w4(W4Args a, cudaStream_t st) {
 
 template <int WPL>
 cudaError_t launch_cols(const W4Args &a, cudaStream_t st) {
-    // fp32 rows take three product columns: 24 columns (three tiles) hold
-    // whole rows
     if (a.cols <= 8) return launch_w4<WPL, 1>(a, st);
     if (a.cols <= 16) return launch_w4<WPL, 2>(a, st);
-    return launch_w4<WPL, 3>(a, st);
+    if (a.cols <= 32) return launch_w4<WPL, 4>(a, st);
+    return launch_w4<WPL, 8>(a, st);
 }
 
 // One thread per (weight row n, group): scale and codes of `group` weights.
@@ -311,11 +452,14 @@ extern "C" ret_status ret_matvec_w4(int M, int N, int K, int group, int x_dtype,
     a.ldx = ldx;
     a.x = X;
     a.xs = codes ? x_scales : nullptr;
+    a.xgrouped = codes && a.xg < K;
     a.wq = static_cast<const uint8_t *>(Wq);
     a.zeros = static_cast<const uint8_t *>(zeros);
     a.s = static_cast<const __nv_bfloat16 *>(scales);
     a.y = Y;
     a.y_bf16 = y_dtype == RET_BF16;
+    const unsigned piece = codes ? 8 : 16;
+    a.vec = aligned(X, piece) && (ldx * xsize) % piece == 0;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const cudaError_t e = group == 128 ? launch_cols<4>(a, st) : group == 64 ? launch_cols<2>(a, st) : launch_cols<1>(a, st);
     return e == cudaSuccess ? RET_OK : RET_ERR_CUDA;
