@@ -658,32 +658,44 @@ _CODES = {torch.float32: RET_F32, torch.bfloat16: RET_BF16, torch.int8: RET_I8,
           torch.float8_e4m3fn: RET_E4M3}
 
 
-def _on(t, name, shape, dtype, device):
-    """Address of a dense tensor of the call's device (None: 0)."""
-    if t is None:
-        return None
+_current_device = torch._C._cuda_getDevice
+_current_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _refuse(t, name, shape, dtype, device):
+    """Raises for a tensor that a call does not take."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.get_device() != device:
         raise TypeError(f"{name} must be a CUDA tensor on device {device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _on(t, name, shape, dtype, device):
+    """Address of a dense tensor of the call's device (None: none)."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.shape != shape or t.get_device() != device or not t.is_contiguous():
+        _refuse(t, name, shape, dtype, device)
     return t.data_ptr()
 
 
 def _rows(t, name, shape, dtype, device):
     """Address and leading dimension of strided rows: unit stride along the
-    last dimension, one stride between all rows before it."""
-    if t.dtype != dtype:
-        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.get_device() != device:
-        raise TypeError(f"{name} must be a CUDA tensor on device {device}")
-    n, stride = shape[-1], t.stride()
-    if n > 1 and stride[-1] != 1:
+    last dimension (or, of [B, L, G, N], dense in the last two), one stride between
+    all rows before it."""
+    if t.dtype != dtype or t.shape != shape or t.get_device() != device:
+        _refuse(t, name, shape, dtype, device)
+    stride, n = t.stride(), shape[-1]
+    if len(shape) == 4:
+        if n > 1 and stride[3] != 1 or shape[2] > 1 and stride[2] != n:
+            raise ValueError(f"{name} needs dense rows of {shape[2]} x {n}")
+        n *= shape[2]
+    elif n > 1 and stride[-1] != 1:
         raise ValueError(f"{name} needs unit stride along its rows")
     if len(shape) == 2:
         ld = stride[0] if shape[0] > 1 else n
@@ -700,17 +712,17 @@ def _rows(t, name, shape, dtype, device):
 
 def _device_of(t, name):
     """Device of a call: the tensor's, which must be the current one."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+    device = t.get_device() if isinstance(t, torch.Tensor) else -1
+    if device < 0:
         raise TypeError(f"{name} must be a CUDA tensor")
-    device = t.get_device()
-    if device != torch.cuda.current_device():
+    if device != _current_device():
         raise ValueError(f"{name} is on device {device}, which is not the current one")
     return device
 
 
 def _on_stream(stream, device):
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(device)
+        return _current_stream(device)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -723,6 +735,8 @@ def ret_rms_norm(X, Y, weight=None, residual=None, residual_out=None, scales=Non
     Returns Y."""
     device = _device_of(X, "X")
     shape = X.shape
+    if not 2 <= len(shape) <= 3:
+        raise ValueError("X must have rows [M, d] or [B, L, d]")
     d = shape[-1]
     px, ldx = _rows(X, "X", shape, X.dtype, device)
     rows = X.numel() // d if d else 0
@@ -791,14 +805,16 @@ def ret_selective_scan(U, delta, A, Bm, Cm, Y, skip=None, Z=None, delta_bias=Non
     shape, dt = U.shape, U.dtype
     B, L, D = shape
     N = A.shape[-1]
-    G = 1 if Bm.dim() == 3 else Bm.shape[2]
-    gn = (B, L, G * N)
-    flat = lambda t: t if t.dim() == 3 else t.flatten(2) if t.stride(2) == N or G == 1 else t  # noqa: E731
+    if Bm.dim() == 3:
+        G, gn = 1, (B, L, N)
+    else:
+        G = Bm.shape[2]
+        gn = (B, L, G, N)
     pu, ldu = _rows(U, "U", shape, dt, device)
     pd, ldd = _rows(delta, "delta", shape, dt, device)
     pz, ldz = (None, 0) if Z is None else _rows(Z, "Z", shape, dt, device)
-    pb, ldb = _rows(flat(Bm), "Bm", gn, dt, device)
-    pc, ldc = _rows(flat(Cm), "Cm", gn, dt, device)
+    pb, ldb = _rows(Bm, "Bm", gn, dt, device)
+    pc, ldc = _rows(Cm, "Cm", gn, dt, device)
     held = (B, D, N)
     desc = RetScanDesc(B, L, D, N, G, _dtype_code(U), int(bool(softplus)), ldu, ldd, ldz, ldb, ldc)
     _check(load_library().ret_selective_scan(
