@@ -527,8 +527,9 @@ ret_status ret_gate_norm_backward(int B, int L, int H, int d_v, int o_dtype,
  * Operands described as "strided rows" are rows of a wider matrix (columns of
  * a projection's output, say): row r starts at base + r*ld elements, ld at
  * least the row's length, and the base need only be aligned to its element.
- * They are read in 16-byte pieces where base and ld are multiples of 16 bytes,
- * element by element otherwise.  Every other pointer is 16-byte aligned, as
+ * They are read fastest where base and ld are multiples of 16 bytes (of 8 for
+ * ret_causal_conv); ret_selective_scan otherwise reads the aligned 16-byte words
+ * that hold a row's elements.  Every other pointer is 16-byte aligned, as
  * above (`lengths`: 4 bytes).  Parameters (norm and convolution weights, A,
  * biases) are fp32.  No output may overlap an input except where said.  All
  * arithmetic is fp32; each output is rounded once.  These calls launch one
@@ -539,6 +540,7 @@ ret_status ret_gate_norm_backward(int B, int L, int H, int d_v, int o_dtype,
 #define RET_MAX_CONV_WIDTH 4     /* taps of ret_causal_conv                  */
 #define RET_MAX_SCAN_STATES 128  /* states per channel of ret_selective_scan */
 #define RET_MAX_MATVEC_ROWS 64   /* rows of one ret_matvec_w4                */
+#define RET_MAX_MATVEC_COLUMNS (1 << 30) /* columns of its result            */
 
 /*
  * ret_rms_norm -- the residual's addition and the root-mean-square norm of
@@ -643,8 +645,8 @@ ret_status ret_selective_scan(const ret_scan_desc *desc, const void *U,
  *   scales  device bf16 [N][K / group]
  *   zeros   device uint8 [N][K / group], 0..15, or NULL (8 everywhere)
  *   Y       device y_dtype (F32, BF16) [M][N]
- * 0 <= M <= RET_MAX_MATVEC_ROWS, group 32, 64 or 128, K a multiple of it.  The
- * products are exact and summed in fp32.  Errors: RET_ERR_NULL, _SHAPE,
+ * 0 <= M <= RET_MAX_MATVEC_ROWS, 0 <= N <= RET_MAX_MATVEC_COLUMNS, group 32, 64
+ * or 128, K a multiple of it.  The products are exact and summed in fp32.  Errors: RET_ERR_NULL, _SHAPE,
  * _DTYPE, _ALIGN, _UNSUPPORTED, _CUDA.
  */
 ret_status ret_matvec_w4(int M, int N, int K, int group, int x_dtype,

@@ -2,19 +2,26 @@
 //     y[m][n] = sum_g s[n][g] sum_{k in g} (q[n][k] - z[n][g]) x[m][k],
 // and ret_quantize_w4, which lays such weights out.
 //
-// Bound by HBM for few rows: the codes are read once.  The products run on the
-// tensor cores' warp-level instruction (m16n8k16, bf16 in, fp32 out): 16 weight
-// rows by 8 columns of x.  Nothing is rounded on the way in: q - z is a small
-// integer, exact in bf16, x is bf16 already, or 8-bit codes (exact in bf16, their
-// scale applied to the sum), or fp32 split into three bf16 parts that add up to
-// it (three columns of the instruction, which has columns to spare).  The sum of
-// a group of weights is scaled in fp32.
+// The products run on the tensor cores' warp-level instruction (m16n8k16, bf16 in,
+// fp32 out): 16 weight rows by 8 columns of x.  Nothing is rounded on the way in:
+// q - z is a small integer, exact in bf16, x is bf16 already, or 8-bit codes (exact
+// in bf16, their scale applied to the sum), or fp32 split into three bf16 parts
+// that add up to it (three columns of the instruction, which has columns to spare).
+// The sum of a group of weights is scaled in fp32.
 //
 // A 32-bit word holds 8 codes of one weight row; masking it at shifts of 0, 4,
 // 8 and 12 bits leaves the pairs (k, k+4), (k+1, k+5), ..., each of which one
 // OR turns into two bf16 values 128 + q.  The instruction sums over k in any
 // order as long as both operands use the same one, so x is kept in shared memory
 // in that order and the codes are never moved between lanes.
+//
+// What bounds it: the floor is HBM, N K / 2 bytes (18.8 us for 8192 x 28672), but
+// turning codes into bf16 takes about 11 instructions a word and the whole loop
+// some 195 a warp and group of 16 x 128 weights, half of them on the integer pipe:
+// 42.7 us for one row there (44% of HBM), 63.6 us for 16 rows of 8-bit codes.  One
+// row times 2048 x 12288: 7.0 us, of which a launch is 2.4.  Measured and not kept:
+// three CTAs an SM at 80 registers (49.6 us for one row: spills), a second chain of
+// products for one column tile alone does not show (kept, 43.2 -> 42.7).
 #include <cuda_fp8.h>
 
 #include <algorithm>
@@ -426,7 +433,7 @@ extern "C" ret_status ret_matvec_w4(int M, int N, int K, int group, int x_dtype,
                                     const void *Wq, const void *scales, const void *zeros,
                                     int y_dtype, void *Y, void *stream) {
     using namespace ret;
-    if (M < 0 || M > RET_MAX_MATVEC_ROWS || N < 0 || K < 1 || ldx < K ||
+    if (M < 0 || M > RET_MAX_MATVEC_ROWS || N < 0 || N > RET_MAX_MATVEC_COLUMNS || K < 1 || ldx < K ||
         (group != 32 && group != 64 && group != 128) || K % group)
         return RET_ERR_SHAPE;
     if (x_dtype < RET_F32 || x_dtype > RET_E4M3 || (y_dtype != RET_F32 && y_dtype != RET_BF16))
@@ -468,7 +475,7 @@ extern "C" ret_status ret_matvec_w4(int M, int N, int K, int group, int x_dtype,
 extern "C" ret_status ret_quantize_w4(int K, int N, int group, int w_dtype, const void *W, long long ldw,
                                       void *Wq, void *scales, void *zeros, void *stream) {
     using namespace ret;
-    if (K < 1 || N < 0 || ldw < N || (group != 32 && group != 64 && group != 128) || K % group)
+    if (K < 1 || N < 0 || N > RET_MAX_MATVEC_COLUMNS || ldw < N || (group != 32 && group != 64 && group != 128) || K % group)
         return RET_ERR_SHAPE;
     if (w_dtype != RET_F32 && w_dtype != RET_BF16) return RET_ERR_DTYPE;
     if (N > 0 && (!W || !Wq || !scales)) return RET_ERR_NULL;

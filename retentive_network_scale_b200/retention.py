@@ -47,6 +47,7 @@ RET_MAX_NORM_WIDTH = 16384
 RET_MAX_CONV_WIDTH = 4
 RET_MAX_SCAN_STATES = 128
 RET_MAX_MATVEC_ROWS = 64
+RET_MAX_MATVEC_COLUMNS = 1 << 30
 
 
 class RetentionError(RuntimeError):

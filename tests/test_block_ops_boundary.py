@@ -92,7 +92,7 @@ def matvec(lib, M=2, N=8, K=128, group=128, xt=BF16, x=FAKE, ldx=128, xs=None, x
 
 @pytest.mark.parametrize("kw,status", [
     (dict(M=-1), "RET_ERR_SHAPE"), (dict(M=R.RET_MAX_MATVEC_ROWS + 1), "RET_ERR_SHAPE"),
-    (dict(N=-1), "RET_ERR_SHAPE"), (dict(K=0), "RET_ERR_SHAPE"), (dict(K=192, ldx=192), "RET_ERR_SHAPE"),
+    (dict(N=-1), "RET_ERR_SHAPE"), (dict(N=R.RET_MAX_MATVEC_COLUMNS + 1), "RET_ERR_SHAPE"), (dict(K=0), "RET_ERR_SHAPE"), (dict(K=192, ldx=192), "RET_ERR_SHAPE"),
     (dict(group=16), "RET_ERR_SHAPE"), (dict(ldx=127), "RET_ERR_SHAPE"),
     (dict(xg=128), "RET_ERR_SHAPE"), (dict(xt=I8, xs=FAKE, xg=64), "RET_ERR_SHAPE"),
     (dict(xt=I8, xs=FAKE, xg=256), "RET_ERR_SHAPE"),

@@ -223,7 +223,8 @@ def check_scan(c, dtype, gate=True, state=True, softplus=True, bare=False, lens=
 @pytest.mark.parametrize("L", [1, 2, 31, 33, 100])
 @pytest.mark.parametrize("D,N,G,pad,off", [(8, 16, 1, 0, 0), (70, 16, 2, 0, 0), (33, 1, 1, 3, 1),
                                            (96, 5, 3, 8, 8), (40, 8, 1, 0, 0), (36, 24, 2, 1, 0),
-                                           (34, 64, 1, 0, 0), (35, 100, 1, 2, 1), (4, 128, 4, 0, 0)])
+                                           (34, 64, 1, 0, 0), (35, 100, 1, 2, 1), (4, 128, 4, 0, 0),
+                                           (160, 16, 2, 0, 0), (48, 32, 3, 8, 8), (32, 120, 2, 8, 0)])
 @pytest.mark.parametrize("dtype", [F32, BF16])
 def test_selective_scan(L, D, N, G, pad, off, dtype):
     c = scan_case(3, L, D, N, G, dtype)
@@ -242,6 +243,48 @@ def test_selective_scan_long(B, L, D):
         c = scan_case(B, L, D, 16, 1, dtype, seed=31)
         check_scan(c, dtype)
         check_scan(c, dtype, state=False, gate=False, lens=[L - 3] + [5] * (B - 1))
+
+
+def test_selective_scan_growing_states():
+    """A above 0 (states that grow), and 0 (that only add up), in one piece and
+    in segments."""
+    for L, D in ((60, 40), (1100, 8)):
+        c = scan_case(2, L, D, 16, 1, F32, seed=45)
+        c["A"][:, 0] = 0.0
+        c["A"][:, 1] = 0.01
+        c["A"][:, 2:] *= 0.1
+        check_scan(c, F32, lens=[L, L - 30])
+
+
+def test_a_call_with_no_rows_passes_the_state_on():
+    s0 = rt((2, 8, 16), 46).cuda()
+    out = torch.empty_like(s0)
+    u, bm = torch.empty(2, 0, 8, device="cuda"), torch.empty(2, 0, 16, device="cuda")
+    A = -torch.ones(8, 16, device="cuda")
+    R.ret_selective_scan(u, u, A, bm, bm, u, state_in=s0, state_out=out)
+    assert torch.equal(out, s0)
+    R.ret_selective_scan(u, u, A, bm, bm, u, state_out=out)
+    assert bool((out == 0).all())
+    held = rt((2, 3, 8), 47).cuda()
+    end = torch.empty_like(held)
+    R.ret_causal_conv(u, torch.ones(8, 4, device="cuda"), u, state_in=held, state_out=end)
+    assert torch.equal(end, held)
+
+
+def test_operands_of_the_scan_at_both_ends_of_an_allocation():
+    """Unaligned rows whose first and last elements are an allocation's: what
+    lies before and behind them in the aligned words does not matter."""
+    B, L, D, N = 1, 21, 13, 3
+    c = scan_case(B, L, D, N, 1, BF16, seed=48)
+    check_scan(c, BF16)
+    wide = torch.full((L * D + 3,), float("nan"), device="cuda", dtype=BF16)
+    u = wide[3:].view(1, L, D)
+    u.copy_(c["u"])
+    y, want = torch.empty(1, L, D, device="cuda", dtype=BF16), torch.empty(1, L, D, device="cuda", dtype=BF16)
+    g = {k: v.cuda() for k, v in c.items()}
+    R.ret_selective_scan(u, g["delta"], g["A"], g["Bm"], g["Cm"], y)
+    R.ret_selective_scan(g["u"], g["delta"], g["A"], g["Bm"], g["Cm"], want)
+    assert torch.equal(y, want)
 
 
 def test_selective_scan_extreme_steps():
