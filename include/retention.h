@@ -660,7 +660,7 @@ ret_status ret_matvec_w4(int M, int N, int K, int group, int x_dtype,
  * scale = max |w| / 7 and code = 8 + round(w / scale); with them, scale =
  * (max - min) / 15 over the group and 0, zero = round(-min / scale).  The codes
  * are taken with the scale as rounded to bf16.
- *   W       device w_dtype (F32, BF16), strided rows: K rows of N values
+ *   W       device w_dtype (F32, BF16), finite, strided rows: K rows of N values
  *   Wq, scales, zeros  device, as ret_matvec_w4 reads them, overwritten; zeros
  *           may be NULL
  * Errors: RET_ERR_NULL, _SHAPE, _DTYPE, _ALIGN, _UNSUPPORTED, _CUDA.

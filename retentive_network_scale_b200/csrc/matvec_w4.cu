@@ -37,6 +37,7 @@ namespace {
 // Threads of a CTA: sixteen warps where the accumulators leave them registers.
 __host__ __device__ constexpr int max_threads(int NT) { return NT <= 2 ? 512 : 256; }
 constexpr size_t kStage = 64 * 1024;  // bytes of x staged at a time
+constexpr int kMaxShared = 2 * kStage;
 constexpr int kSms = 148;
 
 struct W4Args {
@@ -378,8 +379,10 @@ cudaError_t launch_w4(W4Args a, cudaStream_t st) {
     const long long bx = (tiles + a.wr - 1) / a.wr, by = (a.cols + a.tile_cols - 1) / a.tile_cols;
     auto kern = a.zeros ? a.xgrouped ? matvec_w4_kernel<WPL, NT, PF, true, true> : matvec_w4_kernel<WPL, NT, PF, true, false>
                         : a.xgrouped ? matvec_w4_kernel<WPL, NT, PF, false, true> : matvec_w4_kernel<WPL, NT, PF, false, false>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // (the same limit in every call: calls of other sizes may run at once)
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxShared);
     if (e != cudaSuccess) return e;
+    if (smem > (size_t)kMaxShared) return cudaErrorInvalidConfiguration;
     kern<<<dim3((unsigned)bx, (unsigned)by), 32 * a.wr * a.wk, smem, st>>>(a);
     e = cudaGetLastError();
     if (e == cudaSuccess) note_launches(1);

@@ -466,6 +466,41 @@ def test_streams_and_captured_graphs():
     assert all(torch.equal(a, b) for a, b in zip(want, held))
 
 
+def test_calls_of_two_host_threads():
+    """Calls of different sizes of the same kernels at once, each thread on a
+    stream of its own."""
+    import threading
+    jobs, bad = [], []
+    for K, M, L in ((256, 3, 40), (8192, 3, 400)):
+        wq, s, _ = w4_case(48, K, 128, False, seed=85)
+        x = x_case(M, K, BF16, K, seed=86)[0].cuda()
+        c = scan_case(1, L, 24, 16, 1, F32, seed=87)
+        jobs.append((x, wq.cuda(), s.cuda(), {k: v.cuda() for k, v in c.items()}))
+    torch.cuda.synchronize()
+
+    def work(x, wq, s, c):
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            y = [torch.empty(x.shape[0], 48, device="cuda") for _ in range(40)]
+            z = [torch.empty_like(c["u"]) for _ in range(40)]
+            try:
+                for a, b in zip(y, z):
+                    R.ret_matvec_w4(x, wq, s, a)
+                    R.ret_selective_scan(c["u"], c["delta"], c["A"], c["Bm"], c["Cm"], b)
+                stream.synchronize()
+                if not all(torch.equal(a, y[0]) for a in y) or not all(torch.equal(b, z[0]) for b in z):
+                    bad.append("results differ")
+            except Exception as e:  # noqa: BLE001 -- handed to the test's own thread
+                bad.append(repr(e))
+
+    threads = [threading.Thread(target=work, args=j) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad, bad
+
+
 def test_block_serves_a_prompt_and_then_tokens():
     """A block of the operators: norm with the residual, 4-bit projections of
     its 8-bit rows, convolution, scan, 4-bit output projection.  A prompt of 12
