@@ -41,7 +41,7 @@ def build(verbose: bool = False, force: bool = False) -> str:
     if not force and not is_stale():
         return LIB
     nvcc = os.environ.get("NVCC", "nvcc")
-    cmd = [nvcc, *ARCH, "-O3", "-lineinfo", "-std=c++17", "-shared",
+    cmd = [nvcc, *ARCH, "-O3", "-lineinfo", "-std=c++17", "-shared", "--threads", "0",
            "-Xcompiler", "-fPIC,-O2", "-I", INCLUDE, "-I", CSRC,
            *(["-Xptxas", "-v"] if verbose else []),
            *sources(), "-lcublas", "-o", LIB + ".tmp"]
