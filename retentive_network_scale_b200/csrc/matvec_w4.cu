@@ -16,12 +16,13 @@
 // in that order and the codes are never moved between lanes.
 //
 // What bounds it: the floor is HBM, N K / 2 bytes (18.8 us for 8192 x 28672), but
-// turning codes into bf16 takes about 11 instructions a word and the whole loop
-// some 195 a warp and group of 16 x 128 weights, half of them on the integer pipe:
-// 42.7 us for one row there (44% of HBM), 63.6 us for 16 rows of 8-bit codes.  One
-// row times 2048 x 12288: 7.0 us, of which a launch is 2.4.  Measured and not kept:
-// three CTAs an SM at 80 registers (49.6 us for one row: spills), a second chain of
-// products for one column tile alone does not show (kept, 43.2 -> 42.7).
+// turning codes into bf16 takes 11 instructions a word, most of them on the integer
+// pipe, and the loop about as many again: 37.5 us for one row there (50% of HBM),
+// 57.7 us for 16 rows of 8-bit codes.  One row times 2048 x 12288: 6.1 us, of which
+// a launch is 2.4.  The mask and the OR as one three-input operation, which the
+// compiler does not make of them, took the first from 42.7 to 37.5.  Measured and
+// not kept: three CTAs an SM at 80 registers (49.6: spills), shifts as
+// multiplications (46.9), 16 words ahead (the same, but 6.4 us for the small one).
 #include <cuda_fp8.h>
 
 #include <algorithm>
@@ -66,7 +67,8 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
 // it 128 + z): exact.
 template <int J>
 __device__ __forceinline__ uint32_t code_pair(uint32_t w, __nv_bfloat162 zero) {
-    const uint32_t u = ((w >> (4 * J)) & 0x000f000fu) | 0x43004300u;
+    uint32_t u;  // (w >> 4 J & 0x000f000f) | 0x43004300, the last two in one instruction
+    asm("lop3.b32 %0, %1, 0x000f000f, 0x43004300, 0xea;" : "=r"(u) : "r"(w >> (4 * J)));
     const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&u), zero);
     return *reinterpret_cast<const uint32_t *>(&d);
 }
@@ -347,7 +349,7 @@ matvec_w4_kernel(const W4Args a) {
 
 template <int WPL, int NT>
 cudaError_t launch_w4(W4Args a, cudaStream_t st) {
-    constexpr int PF = WPL == 4 ? 4 : 8;  // 16 words a row ahead (8 of the smallest groups)
+    constexpr int PF = 8 / WPL;  // 8 words a row ahead
     const int per = a.x_dtype == RET_F32 ? 3 : 1;
     a.tile_cols = std::min(a.cols, NT * 8 / per * per);  // whole rows of x
     const int groups = a.K / (32 * WPL);
@@ -356,8 +358,9 @@ cudaError_t launch_w4(W4Args a, cudaStream_t st) {
     auto unit = [&](int wk) { return 32 * WPL * PF * wk; };  // columns: one ring of each warp
     // The CTA that leaves the fullest SM least to do, counted in instructions (a
     // group's, x's staging and a CTA's own), each tile of rows shared by as many
-    // warps as fit, down to two groups each.  One token times 2048 x 12288: 6.9 us
-    // with 6 tiles of 2 warps (128 CTAs), 8.2 with 2 of 4, 10.5 with 1 of 8.
+    // warps as fit, down to two groups each.  (One token times 2048 x 12288, before
+    // the unpacking got faster: 6.9 us with 6 tiles of 2 warps (128 CTAs), 8.2 with 2
+    // of 4, 10.5 with 1 of 8.)
     const int most = max_threads(NT) / 32;
     double best = 1e300;
     for (int wr = most; wr >= 1; --wr) {
