@@ -455,7 +455,9 @@ selective_scan_kernel(const ScanArgs a) {
 // sectors) share the channel, and u, d and the step's softplus are worked out once
 // per thread.  Several sequences per thread (A read once for them) measured
 // slower, since the registers cost resident warps: 64 x 4096 x 16 states 13.0 us
-// with four, 10.6 with one.  ONE: L = 1 (9.2 -> 8.6 us for the same).
+// with four, 10.6 with one.  ONE: L = 1 (9.2 -> 8.6 us for the same).  The tiles of
+// 16 rows above took 36 us for one token there, and half of each tile is idle up to
+// kTokenRows.
 constexpr int kTokenRows = 8;  // longest L
 constexpr int kTokenThreads = 128;
 
