@@ -232,12 +232,11 @@ rms_norm_kernel(const NormArgs a) {
 
     const float rs = rsqrtf(ss / (float)a.d + a.eps);
     const float top = a.y_dtype == RET_I8 ? 127.f : 448.f;
-    float factor = rs;
+    float factor = 0.f;  // from y to its codes; 0: the codes are 0
     if (MODE == kRowCodes) {
         float scale;
         group_scale(rs * mx, top, scale, factor);
         if (lane == 0) a.scales[row] = scale;
-        factor *= rs;
     }
 #pragma unroll
     for (int it = 0; it < ITERS; ++it) {
@@ -247,11 +246,15 @@ rms_norm_kernel(const NormArgs a) {
             float scale;
             group_scale(rs * gmax[it], top, scale, factor);
             if (e % a.group == 0) a.scales[row * (a.d / a.group) + e / a.group] = scale;
-            factor *= rs;
         }
         float y[kVec];
 #pragma unroll
-        for (int i = 0; i < H; ++i) v[it][i] = tc::f2_mul(v[it][i], dup(factor));
+        for (int i = 0; i < H; ++i) {
+            // (two products: rs times the factor may lie outside fp32 where y and
+            // its code do not, as for tiny rows and a small eps)
+            v[it][i] = tc::f2_mul(v[it][i], dup(rs));
+            if (MODE != kPlain) v[it][i] = tc::f2_mul(v[it][i], dup(factor));
+        }
         unpack(y, v[it]);
         if (MODE != kPlain && factor == 0.f) {
 #pragma unroll

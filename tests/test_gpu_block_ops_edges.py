@@ -1,0 +1,88 @@
+"""The operators around the mixers on the GPU at the ends of their ranges: tiny and
+non-finite rows, layouts and lengths that take every form of each kernel, streams
+that are not the current one.  References and bounds as in block_ref."""
+import pytest
+import torch
+
+import block_ref as ref
+from retentive_network_scale_b200 import retention as R
+from retentive_network_scale_b200.synth import random_tensor
+
+pytestmark = pytest.mark.gpu
+F32, BF16, I8, E4M3 = torch.float32, torch.bfloat16, torch.int8, torch.float8_e4m3fn
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from retentive_network_scale_b200 import build
+    build.build()
+    R.load_library()
+    yield
+    torch.cuda.synchronize()
+    assert R.ret_last_device_status() == 0
+
+
+def rt(shape, seed, scale=1.0, dtype=F32):
+    return random_tensor(shape, seed, scale).to(dtype)
+
+
+# ------------------------------------------------------------------------ norm
+def check_codes(y, sc, want, g):
+    """Codes and scales of the fp64 rows `want`: the scale within the norm's
+    bound, a value within half a step of its code.  4 NORM: the code is taken of a
+    value and with a scale that are each off."""
+    rows, d = want.shape
+    top = 127.0 if y.dtype == I8 else 448.0
+    scale = want.view(rows, d // g, g).abs().amax(-1) / top
+    assert ref.within(sc, scale, ref.NORM * scale) <= 1
+    got = (y.float().cpu().double().view(rows, d // g, g) * sc.cpu().double()[..., None]).view(rows, d)
+    step = scale.repeat_interleave(g, 1)
+    half = 0.5 * step if y.dtype == I8 else torch.maximum(want.abs() * 2.0 ** -4, step * 2.0 ** -10)
+    assert ref.within(got, want, half + 4 * ref.NORM * (want.abs() + step)) <= 1
+
+
+@pytest.mark.parametrize("group", [0, 32])
+@pytest.mark.parametrize("yt", [I8, E4M3])
+@pytest.mark.parametrize("xs,ws,eps", [(None, 1.0, 1e-6), (1e-10, 1e-27, 0.0), (1e-16, 1.0, 1e-30),
+                                       (1e12, 1e-20, 1e-5)])
+def test_rms_norm_codes_of_tiny_values(group, yt, xs, ws, eps):
+    """The factor between s and its code leaves fp32's range where neither does.
+    (w s may be subnormal: off by 2^-150, which times 1 / rms is under 1e-6 of the
+    step here.)"""
+    rows, d = 3, 96
+    if xs is None:                                      # scales of 2.2e-36, above the least one of 2^-119
+        xs = 2.2e-36 * (127 if yt == I8 else 448) / 1.5 * eps ** 0.5
+    x, w = rt((rows, d), 1).clamp(-1, 1) * xs, 1 + rt((d,), 2, 0.2).clamp(-0.5, 0.5)
+    x[:, ::32] = xs                                     # every group's largest value
+    x[1, 5] = 0.0
+    w[::32] = 1.5
+    w = w * ws
+    y = torch.full((rows, d), 1.0, device="cuda").to(yt)
+    sc = torch.full((rows, d // (group or d)), -1.0, device="cuda")
+    R.ret_rms_norm(x.cuda(), y, weight=w.cuda(), scales=sc, eps=eps)
+    _, want = ref.rms_norm(x, w, None, eps)
+    check_codes(y, sc, want, group or d)
+    assert float(y[1, 5].float()) == 0.0
+
+
+@pytest.mark.parametrize("d,group", [(256, 64), (256, 0), (100, 0), (1056, 32)])
+@pytest.mark.parametrize("yt", [I8, E4M3])
+def test_rms_norm_codes_are_zero_where_the_scale_is_nan(d, group, yt):
+    x = rt((6, d), 3)
+    x[1, 3] = float("nan")
+    x[2, 40] = float("inf")
+    x[3] = 0.0
+    r = torch.zeros(6, d)
+    r[4, 7] = float("nan")
+    for eps in (1e-5, 0.0):
+        y = torch.full((6, d), 1.0, device="cuda").to(yt)
+        sc = torch.zeros(6, d // (group or d), device="cuda")
+        R.ret_rms_norm(x.cuda(), y, residual=r.cuda(), scales=sc, eps=eps)
+        s, code = sc.cpu(), y.float().cpu().view(6, sc.shape[1], -1)
+        assert bool(torch.isnan(s[[1, 4]]).all())               # the sum of squares is NaN
+        assert bool(torch.isnan(s[2, 40 // (group or d)]))      # infinity over an infinite norm
+        assert bool(torch.isnan(s[3]).all()) == (eps == 0.0)    # 0 / 0
+        assert bool(torch.isfinite(s[[0, 5]]).all())
+        dead = torch.isnan(s) | (s == 0)
+        assert bool((code[dead] == 0).all()) and not bool(torch.isnan(code).any())
+        assert bool((code[[0, 5]].abs().amax(-1) > 0).all())
