@@ -135,16 +135,17 @@ __device__ __forceinline__ void store8_codes(uint8_t *p, const float *v, int n, 
 }
 
 // The scale of a group whose largest |y| is m, and the factor that takes y to its
-// codes.  All-zero group: 0 and 0.  A value that is not finite: NaN and 0.
+// codes.  All-zero group, or a scale below 2^-119: 0 and 0.  A value that is not
+// finite: NaN and 0.
 __device__ __forceinline__ void group_scale(float m, float top, float &scale, float &factor) {
     if (!(m <= 3.4028235e38f)) {
         scale = __uint_as_float(0x7fc00000u);
         factor = 0.f;
     } else {
+        // from 2^-119 on the scale, the factor (at most 2^119) and a code times
+        // the scale (e4m3: down to 2^-9 of it) are normal numbers
         scale = m / top;
-        // top / m overflows for m below about 2^-119; such codes are lost
-        // with the scale's own precision (it is denormal there)
-        factor = scale > 1.2e-36f ? top / m : 0.f;
+        factor = scale >= 0x1p-119f ? top / m : 0.f;
         if (factor == 0.f) scale = 0.f;
     }
 }

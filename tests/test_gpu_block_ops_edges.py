@@ -86,3 +86,20 @@ def test_rms_norm_codes_are_zero_where_the_scale_is_nan(d, group, yt):
         dead = torch.isnan(s) | (s == 0)
         assert bool((code[dead] == 0).all()) and not bool(torch.isnan(code).any())
         assert bool((code[[0, 5]].abs().amax(-1) > 0).all())
+
+
+@pytest.mark.parametrize("yt", [I8, E4M3])
+def test_rms_norm_least_scale(yt):
+    """A scale below 2^-119 is 0, with codes 0; one above is kept."""
+    d, top = 64, 127.0 if yt == I8 else 448.0
+    limit = 2.0 ** -119
+    x = torch.zeros(4, d)
+    # eps = 1 gives y = s; 2^-20 is far above the norm's bound
+    for row, f in enumerate((0.81, 1 - 2.0 ** -20, 1 + 2.0 ** -20, 1.2)):
+        x[row, ::3] = limit * top * f
+    y, sc = torch.full((4, d), 1.0, device="cuda").to(yt), torch.full((4, 1), -1.0, device="cuda")
+    R.ret_rms_norm(x.cuda(), y, scales=sc, eps=1.0)
+    codes, s = y.float().cpu(), sc.cpu()[:, 0]
+    assert s[:2].tolist() == [0.0, 0.0] and bool((codes[:2] == 0).all())
+    assert bool((s[2:] >= limit).all()) and bool((codes[2:, ::3] == top).all())
+    assert ref.within(s[2:], x[2:, 0].double() / top, ref.NORM * x[2:, 0].double() / top) <= 1
