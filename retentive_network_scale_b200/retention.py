@@ -202,6 +202,21 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
+def _empty(shape, dtype, device, stream):
+    """torch.empty for what a call makes itself, in the memory of the stream that
+    the call runs on: a block that the allocator holds for another stream (the
+    current one) may still be in use there, and may be handed out there again before
+    the call's kernels are done with it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream(stream).value or 0
+        # (1 is the default stream's other handle)
+        stream = torch.cuda.ExternalStream(0 if handle == 1 else handle, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def make_desc(B, H, L, d_k, d_v, in_dtype, out_dtype, gamma, rotate=False,
               theta_base=10000.0, pos_offset=0):
     if len(gamma) != H:
@@ -870,10 +885,10 @@ def ret_quantize_w4(W, group, zeros=False, stream=None):
     device = _device_of(W, "W")
     K, N = W.shape
     pw, ldw = _rows(W, "W", W.shape, W.dtype, device)
-    wq = torch.empty(N, K // 2, device=W.device, dtype=torch.uint8)
+    wq = _empty((N, K // 2), torch.uint8, W.device, stream)
     groups = K // group if group > 0 else 0
-    scales = torch.empty(N, groups, device=W.device, dtype=torch.bfloat16)
-    zp = torch.empty(N, groups, device=W.device, dtype=torch.uint8) if zeros else None
+    scales = _empty((N, groups), torch.bfloat16, W.device, stream)
+    zp = _empty((N, groups), torch.uint8, W.device, stream) if zeros else None
     _check(load_library().ret_quantize_w4(K, N, int(group), _dtype_code(W), pw, ldw, wq.data_ptr(),
                                           scales.data_ptr(), None if zp is None else zp.data_ptr(),
                                           _on_stream(stream, device)), "ret_quantize_w4")

@@ -1,0 +1,67 @@
+"""What the binding does on the host around the calls of the operators, checked
+without a GPU: the library and torch's streams are stood in for."""
+import contextlib
+
+import pytest
+import torch
+
+from retentive_network_scale_b200 import retention as R
+
+
+class FakeLibrary:
+    """Every entry point succeeds, every size is `need` bytes."""
+
+    def __init__(self, need=64):
+        self.need, self.calls = need, []
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.calls.append(name)
+            return self.need if name.endswith("_size") else 0
+        return call
+
+
+@pytest.fixture
+def streams(monkeypatch):
+    """Stands in for torch's streams; returns the (stream, bytes) of each allocation
+    (the stream being None for the current one)."""
+    inside, made, empty = [None], [], torch.empty
+
+    class Stream:
+        def __init__(self, handle=0, device=None):
+            self.cuda_stream = handle
+
+    @contextlib.contextmanager
+    def use(stream):
+        inside.append(stream)
+        yield
+        inside.pop()
+
+    def allocate(*shape, **kw):
+        kw["device"] = "cpu"
+        t = empty(*shape, **kw)
+        made.append((inside[-1], t.numel() * t.element_size()))
+        return t
+
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", Stream)
+    monkeypatch.setattr(torch.cuda, "stream", use)
+    monkeypatch.setattr(torch, "empty", allocate)
+    monkeypatch.setattr(R, "load_library", lambda *a: FakeLibrary())
+    monkeypatch.setattr(R, "_device_of", lambda t, name: 0)
+    monkeypatch.setattr(R, "_rows", lambda t, name, shape, dtype, device: (0x1000, shape[-1]))
+    monkeypatch.setattr(R, "_on_stream", lambda stream, device: 0)
+    return made
+
+
+def test_quantize_w4_makes_its_results_on_its_stream(streams):
+    W = torch.zeros(128, 8)
+    side = torch.cuda.Stream(0x40)
+    R.ret_quantize_w4(W, 64, zeros=True, stream=side)
+    assert [s for s, _ in streams] == [side] * 3
+    streams.clear()
+    R.ret_quantize_w4(W, 64, zeros=True, stream=0x80)           # a raw handle
+    assert [s.cuda_stream for s, _ in streams] == [0x80] * 3
+    streams.clear()
+    R.ret_quantize_w4(W, 64)
+    assert streams == [(None, 8 * 64), (None, 8 * 2 * 2)]

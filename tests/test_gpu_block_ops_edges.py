@@ -103,3 +103,29 @@ def test_rms_norm_least_scale(yt):
     assert s[:2].tolist() == [0.0, 0.0] and bool((codes[:2] == 0).all())
     assert bool((s[2:] >= limit).all()) and bool((codes[2:, ::3] == top).all())
     assert ref.within(s[2:], x[2:, 0].double() / top, ref.NORM * x[2:, 0].double() / top) <= 1
+
+
+# ------------------------------------------------------------------------ streams
+def busy_then_freed(shapes):
+    """Blocks of these (shape, dtype) that the allocator holds for the current
+    stream, where work that writes them is still to come."""
+    torch.cuda.synchronize()
+    held = [torch.empty(shape, device="cuda", dtype=dtype) for shape, dtype in shapes]
+    torch.cuda._sleep(int(5e7))                         # some 25 ms
+    for t in held:
+        t.fill_(3)
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_quantize_w4_on_another_stream(raw):
+    K, N, g = 1024, 2048, 64
+    W = rt((K, N), 11).cuda()
+    want = R.ret_quantize_w4(W, g, zeros=True)
+    side = torch.cuda.Stream()
+    busy_then_freed([(t.shape, t.dtype) for t in want])
+    got = R.ret_quantize_w4(W, g, zeros=True, stream=side.cuda_stream if raw else side)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    if raw:     # the default stream's handles
+        for handle in (0, 1):
+            assert all(torch.equal(a, b) for a, b in zip(want, R.ret_quantize_w4(W, g, True, stream=handle)))
