@@ -249,7 +249,7 @@ def ret_parallel(Q, K, V, O, gamma, rotate=False, theta_base=10000.0, pos_offset
                   theta_base, pos_offset)
     need = int(lib.ret_parallel_workspace_size(ctypes.byref(d)))
     if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=Q.device)
+        workspace = _empty(need, torch.uint8, Q.device, stream)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(lib.ret_parallel(ctypes.byref(d), _ptr(Q), _ptr(K), _ptr(V), _ptr(O),
                             _ptr(workspace), ws_bytes, _stream(stream)), "ret_parallel")
@@ -356,7 +356,7 @@ def ret_chunkwise_host(Q, K, V, gamma, chunk, O=None, G=None, Y=None, gn_eps=1e-
     need = int(lib.ret_chunkwise_host_workspace_size(ctypes.byref(d), int(chunk), int(O is not None),
                                                      int(Y is not None), max(slices, 1)))
     if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device="cuda")
+        workspace = _empty(need, torch.uint8, "cuda", stream)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(lib.ret_chunkwise_host(ctypes.byref(d), int(chunk), _ptr(Q), _ptr(K), _ptr(V), _ptr(O),
                                   _ptr(G), float(gn_eps), _ptr(Y), slices, _ptr(workspace), ws_bytes,
@@ -386,12 +386,12 @@ def ret_msr_layer(X, W_qkvg, W_o, gamma, chunk, d_k, d_v, out=None, gn_eps=1e-5,
     _dev(X, "X", dtype=torch.bfloat16); _dev(W_qkvg, "W_qkvg", (dm, n_proj), torch.bfloat16)
     _dev(W_o, "W_o", (H * d_v, dm), torch.bfloat16)
     if out is None:
-        out = torch.empty(B, L, dm, device=X.device, dtype=torch.bfloat16)
+        out = _empty((B, L, dm), torch.bfloat16, X.device, stream)
     _dev(out, "out", (B, L, dm), torch.bfloat16)
     d = make_desc(B, H, L, d_k, d_v, RET_BF16, RET_BF16, gamma, rotate, theta_base, pos_offset)
     need = int(lib.ret_msr_layer_workspace_size(ctypes.byref(d), int(dm), int(chunk)))
     if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=X.device)
+        workspace = _empty(need, torch.uint8, X.device, stream)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(lib.ret_msr_layer(ctypes.byref(d), int(dm), int(chunk), _ptr(X), _ptr(W_qkvg), _ptr(W_o),
                              float(gn_eps), _ptr(out), _ptr(workspace), ws_bytes, _stream(stream)),
@@ -413,7 +413,7 @@ def ret_gemm_bf16(A, B, C=None, stream=None):
     if K2 != K:
         raise ValueError("inner sizes differ")
     if C is None:
-        C = torch.empty(M, N, device=A.device, dtype=torch.bfloat16)
+        C = _empty((M, N), torch.bfloat16, A.device, stream)
     if not C.is_cuda or C.dim() != 2 or C.stride(1) != 1 or tuple(C.shape) != (M, N) \
             or C.dtype != torch.bfloat16:
         raise ValueError("C must be a 2-D bf16 CUDA tensor [M, N] with unit row stride")
@@ -439,14 +439,14 @@ def ret_backward(Q, K, V, dO, gamma, chunk, dQ=None, dK=None, dV=None, out_dtype
     dv = V.shape[-1]
     _dev(Q, "Q", dtype=torch.bfloat16); _dev(K, "K", Q.shape, torch.bfloat16)
     _dev(V, "V", (B, H, L, dv), torch.bfloat16); _dev(dO, "dO", (B, H, L, dv), torch.bfloat16)
-    mk = lambda t, shape: t if t is not None else torch.empty(shape, device=Q.device, dtype=out_dtype)  # noqa: E731
+    mk = lambda t, shape: t if t is not None else _empty(shape, out_dtype, Q.device, stream)  # noqa: E731
     dQ, dK, dV = mk(dQ, (B, H, L, dk)), mk(dK, (B, H, L, dk)), mk(dV, (B, H, L, dv))
     _dev(dQ, "dQ", (B, H, L, dk)); _dev(dK, "dK", (B, H, L, dk), dQ.dtype)
     _dev(dV, "dV", (B, H, L, dv), dQ.dtype)
     d = make_desc(B, H, L, dk, dv, RET_BF16, _dtype_code(dQ), gamma, rotate, theta_base, pos_offset)
     need = int(lib.ret_backward_workspace_size(ctypes.byref(d), int(chunk)))
     if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=Q.device)
+        workspace = _empty(need, torch.uint8, Q.device, stream)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(lib.ret_backward(ctypes.byref(d), int(chunk), _ptr(Q), _ptr(K), _ptr(V), _ptr(dO), _ptr(dQ),
                             _ptr(dK), _ptr(dV), _ptr(workspace), ws_bytes, _stream(stream)),
@@ -471,12 +471,12 @@ def ret_segment_state(K, V, gamma, U=None, rotate=False, theta_base=10000.0, pos
     dv = V.shape[-1]
     _dev(K, "K", dtype=torch.bfloat16); _dev(V, "V", (B, H, L, dv), torch.bfloat16)
     if U is None:
-        U = torch.empty(B, H, dk, dv, device=K.device, dtype=torch.float32)
+        U = _empty((B, H, dk, dv), torch.float32, K.device, stream)
     _dev(U, "U", (B, H, dk, dv), torch.float32)
     d = make_desc(B, H, L, dk, dv, RET_BF16, RET_F32, gamma, rotate, theta_base, pos_offset)
     need = int(lib.ret_segment_state_workspace_size(ctypes.byref(d)))
     if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=K.device)
+        workspace = _empty(need, torch.uint8, K.device, stream)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(lib.ret_segment_state(ctypes.byref(d), _ptr(K), _ptr(V), _ptr(U), _ptr(workspace),
                                  ws_bytes, _stream(stream)), "ret_segment_state")
@@ -500,7 +500,7 @@ def ret_state_scan(U_all, seg_lens, rank, gamma, state_in=None, R=None, stream=N
     if state_in is not None:
         _dev(state_in, "state_in", (B, H, dk, dv), torch.float32)
     if R is None:
-        R = torch.empty(B, H, dk, dv, device=U_all.device, dtype=torch.float32)
+        R = _empty((B, H, dk, dv), torch.float32, U_all.device, stream)
     _dev(R, "R", (B, H, dk, dv), torch.float32)
     lens = (ctypes.c_int * len(seg_lens))(*[int(x) for x in seg_lens])
     d = make_desc(B, H, 0, dk, dv, RET_F32, RET_F32, gamma)
@@ -522,14 +522,14 @@ def ret_chunkwise_segmented(Q, K, V, gamma, chunk, segments, O=None, state_in=No
     _dev(Q, "Q", dtype=torch.bfloat16); _dev(K, "K", Q.shape, torch.bfloat16)
     _dev(V, "V", (B, H, L, dv), torch.bfloat16)
     if O is None:
-        O = torch.empty(B, H, L, dv, device=Q.device, dtype=out_dtype)
+        O = _empty((B, H, L, dv), out_dtype, Q.device, stream)
     _dev(O, "O", (B, H, L, dv))
     _dev(state_in, "state_in", (B, H, dk, dv), torch.float32)
     _dev(state_out, "state_out", (B, H, dk, dv), torch.float32)
     d = make_desc(B, H, L, dk, dv, RET_BF16, _dtype_code(O), gamma, rotate, theta_base, pos_offset)
     need = int(lib.ret_chunkwise_segmented_workspace_size(ctypes.byref(d), int(chunk), int(segments)))
     if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=Q.device)
+        workspace = _empty(need, torch.uint8, Q.device, stream)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(lib.ret_chunkwise_segmented(ctypes.byref(d), int(chunk), int(segments), _ptr(Q), _ptr(K),
                                        _ptr(V), _ptr(state_in), _ptr(state_out), _ptr(O),
@@ -591,7 +591,7 @@ def ret_chunkwise(Q, K, V, gamma, chunk, O=None, state_in=None, state_out=None, 
     if prep:
         need = max(need, int(lib.ret_chunkwise_fast_size(ctypes.byref(d), int(chunk))))
     if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=Q.device)
+        workspace = _empty(need, torch.uint8, Q.device, stream)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(lib.ret_chunkwise(ctypes.byref(d), int(chunk), _ptr(Q), _ptr(K), _ptr(V),
                              _ptr(state_in), _ptr(state_out), _ptr(O), _ptr(G),

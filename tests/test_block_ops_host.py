@@ -65,3 +65,31 @@ def test_quantize_w4_makes_its_results_on_its_stream(streams):
     streams.clear()
     R.ret_quantize_w4(W, 64)
     assert streams == [(None, 8 * 64), (None, 8 * 2 * 2)]
+
+
+def test_workspaces_and_results_of_every_call_are_made_on_its_stream(streams, monkeypatch):
+    """The kernels of a call on `stream` use them after the call has returned and
+    let go of them."""
+    monkeypatch.setattr(R, "_dev", lambda t, *a, **k: t)
+    B, H, L, dk, dv, chunk, gamma = 1, 2, 8, 4, 4, 4, [0.9, 0.8]
+    q, v = torch.zeros(B, H, L, dk), torch.zeros(B, H, L, dv)
+    b, bv, G = q.bfloat16(), v.bfloat16(), torch.zeros(B, L, H * dv)
+    x, w = torch.zeros(B, L, 8).bfloat16(), torch.zeros(8, H * (2 * dk + 2 * dv)).bfloat16()
+    w_o, U = torch.zeros(H * dv, 8).bfloat16(), torch.zeros(2, B, H, dk, dv)
+    calls = [
+        (1, lambda s: R.ret_parallel(q, q, v, v, gamma, stream=s)),
+        (1, lambda s: R.ret_chunkwise(q, q, v, gamma, chunk, O=v, stream=s)),
+        (1, lambda s: R.ret_chunkwise_host(q, q, v, gamma, chunk, O=v, stream=s)),
+        (2, lambda s: R.ret_msr_layer(x, w, w_o, gamma, chunk, dk, dv, stream=s)),
+        (4, lambda s: R.ret_backward(b, b, bv, bv, gamma, chunk, stream=s)),
+        (2, lambda s: R.ret_segment_state(b, bv, gamma, stream=s)),
+        (1, lambda s: R.ret_state_scan(U, [4, 4], 1, gamma, stream=s)),
+        (2, lambda s: R.ret_chunkwise_segmented(b, b, bv, gamma, chunk, 2, stream=s)),
+    ]
+    monkeypatch.setattr(R, "_stream", lambda s: R.ctypes.c_void_p(0))
+    side = torch.cuda.Stream(0x40)
+    for n, call in calls:
+        for stream in (side, None):
+            streams.clear()
+            call(stream)
+            assert [s for s, _ in streams] == [stream] * n

@@ -129,3 +129,35 @@ def test_quantize_w4_on_another_stream(raw):
     if raw:     # the default stream's handles
         for handle in (0, 1):
             assert all(torch.equal(a, b) for a, b in zip(want, R.ret_quantize_w4(W, g, True, stream=handle)))
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_calls_with_workspaces_on_another_stream(raw):
+    """A workspace or result that the call makes is neither taken from nor given
+    back to the current stream while the call's kernels run elsewhere."""
+    B, H, L, dk, dv, chunk, gamma = 2, 4, 512, 128, 128, 64, [0.95, 0.97, 0.98, 0.99]
+    q, k = (rt((B, H, L, dk), s, dk ** -0.5, BF16).cuda() for s in (12, 13))
+    v, do = (rt((B, H, L, dv), s, 1.0, BF16).cuda() for s in (14, 15))
+    a, b = rt((512, 256), 16, 1.0, BF16).cuda(), rt((256, 512), 17, 1.0, BF16).cuda()
+    o = torch.empty_like(v)
+    calls = [lambda s: R.ret_parallel(q, k, v, o, gamma, stream=s),
+             lambda s: R.ret_chunkwise(q, k, v, gamma, chunk, O=o, stream=s)[0],
+             lambda s: R.ret_backward(q, k, v, do, gamma, chunk, stream=s),
+             lambda s: R.ret_segment_state(k, v, gamma, stream=s),
+             lambda s: R.ret_chunkwise_segmented(q, k, v, gamma, chunk, 4, stream=s)[0],
+             lambda s: R.ret_gemm_bf16(a, b, stream=s)]
+    side = torch.cuda.Stream()
+    for call in calls:
+        whole = lambda t: [x.clone() for x in (t if isinstance(t, tuple) else (t,))]  # noqa: E731
+        want = whole(call(None))
+        torch.cuda.synchronize()
+        o.zero_()
+        busy_then_freed([(t.shape, t.dtype) for t in want])
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(int(5e7))
+        got = call(side.cuda_stream if raw else side)
+        # what the call has let go of must not come back here before it is done
+        blocks = [torch.full((n,), 255, device="cuda", dtype=torch.uint8) for n in (1 << 14, 1 << 18, 1 << 20, 1 << 22, 1 << 24)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(want, whole(got)))
+        del blocks
