@@ -674,8 +674,10 @@ _CODES = {torch.float32: RET_F32, torch.bfloat16: RET_BF16, torch.int8: RET_I8,
           torch.float8_e4m3fn: RET_E4M3}
 
 
-_current_device = torch._C._cuda_getDevice
-_current_stream = torch._C._cuda_getCurrentRawStream
+# torch's own shortcuts, which a torch built without CUDA lacks
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                          lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
 def _refuse(t, name, shape, dtype, device):

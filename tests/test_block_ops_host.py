@@ -1,6 +1,7 @@
 """What the binding does on the host around the calls of the operators, checked
 without a GPU: the library and torch's streams are stood in for."""
 import contextlib
+import importlib.util
 
 import pytest
 import torch
@@ -93,3 +94,15 @@ def test_workspaces_and_results_of_every_call_are_made_on_its_stream(streams, mo
             streams.clear()
             call(stream)
             assert [s for s, _ in streams] == [stream] * n
+
+
+def test_binding_imports_on_a_torch_without_cuda(monkeypatch):
+    for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"):
+        monkeypatch.delattr(torch._C, name, raising=False)
+    spec = importlib.util.spec_from_file_location("retention_without_cuda", R.__file__)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    with pytest.raises(TypeError):
+        module.ret_rms_norm(torch.zeros(2, 8), torch.zeros(2, 8))
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device: type("S", (), dict(cuda_stream=7)))
+    assert module._on_stream(None, 0) == 7
