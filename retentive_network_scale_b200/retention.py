@@ -693,11 +693,19 @@ def _refuse(t, name, shape, dtype, device):
     raise ValueError(f"{name} must be contiguous")
 
 
+def _tensor(t, name, *dims):
+    """Raises unless t is a tensor of one of these numbers of dimensions."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dim() not in dims:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {' or '.join(map(str, dims))} dimensions")
+
+
 def _on(t, name, shape, dtype, device):
     """Address of a dense tensor of the call's device (None: none)."""
     if t is None:
         return None
-    if t.dtype != dtype or t.shape != shape or t.get_device() != device or not t.is_contiguous():
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape or t.get_device() != device or not t.is_contiguous():
         _refuse(t, name, shape, dtype, device)
     return t.data_ptr()
 
@@ -706,7 +714,7 @@ def _rows(t, name, shape, dtype, device):
     """Address and leading dimension of strided rows: unit stride along the
     last dimension (or, of [B, L, G, N], dense in the last two), one stride between
     all rows before it."""
-    if t.dtype != dtype or t.shape != shape or t.get_device() != device:
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape or t.get_device() != device:
         _refuse(t, name, shape, dtype, device)
     stride, n = t.stride(), shape[-1]
     if len(shape) == 4:
@@ -752,9 +760,10 @@ def ret_rms_norm(X, Y, weight=None, residual=None, residual_out=None, scales=Non
     scales [.., groups] (fp32): one per row, or per 32, 64 or 128 channels.
     Returns Y."""
     device = _device_of(X, "X")
+    _tensor(X, "X", 2, 3)
     shape = X.shape
-    if not 2 <= len(shape) <= 3:
-        raise ValueError("X must have rows [M, d] or [B, L, d]")
+    dims = len(shape)
+    _tensor(Y, "Y", dims)
     d = shape[-1]
     px, ldx = _rows(X, "X", shape, X.dtype, device)
     rows = X.numel() // d if d else 0
@@ -765,6 +774,7 @@ def ret_rms_norm(X, Y, weight=None, residual=None, residual_out=None, scales=Non
     if y_dtype >= RET_I8:
         if scales is None:
             raise ValueError("an 8-bit Y needs scales")
+        _tensor(scales, "scales", dims)
         groups = scales.shape[-1]
         if groups < 1 or d % groups:
             raise ValueError("scales must divide the channels into equal groups")
@@ -775,9 +785,8 @@ def ret_rms_norm(X, Y, weight=None, residual=None, residual_out=None, scales=Non
     else:
         ps = None
     if residual is not None:
+        _tensor(residual, "residual", dims)
         r_dtype = _dtype_code(residual)
-        if residual_out is not None and residual_out.dtype != residual.dtype:
-            raise TypeError("residual_out takes residual's dtype")
     elif residual_out is not None:
         raise ValueError("residual_out needs residual")
     _check(load_library().ret_rms_norm(
@@ -798,6 +807,8 @@ def ret_causal_conv(X, weight, Y, bias=None, swish=True, lengths=None, state_in=
     both updates it in place; L = 1 is a single token), lengths [B] (int32) the
     valid rows of a padded batch.  Returns (Y, state_out)."""
     device = _device_of(X, "X")
+    _tensor(X, "X", 3)
+    _tensor(weight, "weight", 2)
     B, L, D = X.shape
     width = weight.shape[-1]
     dt = X.dtype
@@ -820,6 +831,9 @@ def ret_selective_scan(U, delta, A, Bm, Cm, Y, skip=None, Z=None, delta_bias=Non
     L = 1 is a single token), lengths [B] (int32) the valid rows of a padded
     batch.  Returns (Y, state_out)."""
     device = _device_of(U, "U")
+    _tensor(U, "U", 3)
+    _tensor(A, "A", 2)
+    _tensor(Bm, "Bm", 3, 4)
     shape, dt = U.shape, U.dtype
     B, L, D = shape
     N = A.shape[-1]
@@ -852,6 +866,9 @@ def ret_matvec_w4(X, Wq, scales, Y, zeros=None, x_scales=None, stream=None):
     [N,K/2] (uint8) with scales [N,K/group] (bfloat16) and zeros (uint8, same
     shape).  Returns Y."""
     device = _device_of(X, "X")
+    _tensor(X, "X", 2)
+    _tensor(scales, "scales", 2)
+    _tensor(Y, "Y", 2)
     M, K = X.shape
     N, groups = scales.shape
     x_dtype = _CODES.get(X.dtype)
@@ -864,6 +881,7 @@ def ret_matvec_w4(X, Wq, scales, Y, zeros=None, x_scales=None, stream=None):
     if x_dtype >= RET_I8:
         if x_scales is None:
             raise ValueError("8-bit rows need x_scales")
+        _tensor(x_scales, "x_scales", 2)
         n = x_scales.shape[-1]
         if n < 1 or K % n:
             raise ValueError("x_scales must divide the columns into equal groups")
@@ -885,6 +903,7 @@ def ret_quantize_w4(W, group, zeros=False, stream=None):
     with `zeros`, a zero point) per `group` rows of each column.  Returns
     (Wq [N,K/2] uint8, scales [N,K/group] bfloat16, zeros uint8 or None)."""
     device = _device_of(W, "W")
+    _tensor(W, "W", 2)
     K, N = W.shape
     pw, ldw = _rows(W, "W", W.shape, W.dtype, device)
     wq = _empty((N, K // 2), torch.uint8, W.device, stream)

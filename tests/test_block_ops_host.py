@@ -106,3 +106,47 @@ def test_binding_imports_on_a_torch_without_cuda(monkeypatch):
         module.ret_rms_norm(torch.zeros(2, 8), torch.zeros(2, 8))
     monkeypatch.setattr(torch.cuda, "current_stream", lambda device: type("S", (), dict(cuda_stream=7)))
     assert module._on_stream(None, 0) == 7
+
+
+def block_calls():
+    """A valid call of each operator, as (function, arguments by name); host
+    tensors."""
+    z, bf, i8 = torch.zeros, torch.bfloat16, torch.int8
+    x = z(2, 8, 64)
+    return [
+        (R.ret_rms_norm, dict(X=x, Y=z(2, 8, 64, dtype=i8), weight=z(64), residual=x.to(bf),
+                              residual_out=x.to(bf), scales=z(2, 8, 2))),
+        (R.ret_causal_conv, dict(X=x, weight=z(64, 4), Y=z(2, 8, 64), bias=z(64), lengths=z(2, dtype=torch.int32),
+                                 state_in=z(2, 3, 64), state_out=z(2, 3, 64))),
+        (R.ret_selective_scan, dict(U=x, delta=x, A=z(64, 16), Bm=z(2, 8, 2, 16), Cm=z(2, 8, 2, 16), Y=z(2, 8, 64),
+                                    skip=z(64), Z=x, delta_bias=z(64), lengths=z(2, dtype=torch.int32),
+                                    state_in=z(2, 64, 16), state_out=z(2, 64, 16))),
+        (R.ret_matvec_w4, dict(X=z(3, 64, dtype=i8), Wq=z(8, 32, dtype=torch.uint8), scales=z(8, 2, dtype=bf),
+                               Y=z(3, 8), zeros=z(8, 2, dtype=torch.uint8), x_scales=z(3, 1))),
+        (R.ret_quantize_w4, dict(W=z(64, 8), group=32)),
+    ]
+
+
+@pytest.mark.parametrize("fn,args", block_calls(), ids=lambda v: getattr(v, "__name__", ""))
+def test_block_calls_refuse_what_is_not_a_tensor_of_the_shape(monkeypatch, fn, args):
+    lib = FakeLibrary()
+    monkeypatch.setattr(R, "load_library", lambda *a: lib)
+    monkeypatch.setattr(R, "_device_of", lambda t, name: -1)    # the host's number
+    monkeypatch.setattr(R, "_on_stream", lambda stream, device: 0)
+    fn(**args)
+    assert lib.calls == [fn.__name__]
+    for name, t in args.items():
+        if not isinstance(t, torch.Tensor):
+            continue
+        if name not in ("X", "U", "W"):         # those are looked at by _device_of
+            for wrong in (t.numpy() if t.dtype != torch.bfloat16 else t.float().numpy(), t.tolist(), 1.0):
+                with pytest.raises(TypeError):
+                    fn(**dict(args, **{name: wrong}))
+        for wrong in (t[..., 0] if name != "Bm" else t[..., 0, 0], t[..., None] if t.dim() < 4 else t[..., None, None],
+                      torch.zeros((), dtype=t.dtype)):
+            with pytest.raises(ValueError):
+                fn(**dict(args, **{name: wrong}))
+        if name != "W":
+            with pytest.raises(TypeError):
+                fn(**dict(args, **{name: t.to(torch.float64)}))
+    assert lib.calls == [fn.__name__]
