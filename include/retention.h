@@ -646,8 +646,10 @@ ret_status ret_selective_scan(const ret_scan_desc *desc, const void *U,
  *   zeros   device uint8 [N][K / group], 0..15, or NULL (8 everywhere)
  *   Y       device y_dtype (F32, BF16) [M][N]
  * 0 <= M <= RET_MAX_MATVEC_ROWS, 0 <= N <= RET_MAX_MATVEC_COLUMNS, group 32, 64
- * or 128, K a multiple of it.  The products are exact and summed in fp32.  Errors: RET_ERR_NULL, _SHAPE,
- * _DTYPE, _ALIGN, _UNSUPPORTED, _CUDA.
+ * or 128, K a multiple of it.  The products (q - zero) x are exact, but that of an
+ * fp32 x what lies below 2^-133 is lost; they are summed in fp32, a group's before
+ * its scale is applied (so a finite y may still come from sums past fp32's range
+ * as infinity).  Errors: RET_ERR_NULL, _SHAPE, _DTYPE, _ALIGN, _UNSUPPORTED, _CUDA.
  */
 ret_status ret_matvec_w4(int M, int N, int K, int group, int x_dtype,
                          const void *X, long long ldx, const float *x_scales,

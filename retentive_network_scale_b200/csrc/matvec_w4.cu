@@ -123,8 +123,10 @@ __device__ __forceinline__ void load_x(const W4Args &a, RawX &r, int m, int k) {
         r.q[0].y = u.y;
     }
 }
-// Them as bf16 pairs (j, j + 4): for fp32 rows the three parts of 8 bits each,
-// dst[0], dst[4] and dst[8].
+// Them as bf16 pairs (j, j + 4): for fp32 rows the three parts that the 24 bits of a
+// value are cut into, 8 bits each, dst[0], dst[4] and dst[8].  Cut, not rounded: a
+// first part rounded up could be infinite.  (What is below 2^-133, the least bf16,
+// is lost.)
 __device__ __forceinline__ void stage_x(const W4Args &a, const RawX &r, uint4 *dst) {
     const uint4 u = r.q[0], t = r.q[1];
     if (a.x_dtype == RET_BF16) {
@@ -137,13 +139,15 @@ __device__ __forceinline__ void stage_x(const W4Args &a, const RawX &r, uint4 *d
         for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(bits[i]);
 #pragma unroll
         for (int j = 0; j < 3; ++j) {
-            const uint4 p = pack_x(v);
-            dst[4 * j] = p;
-            const uint32_t w[4] = {p.x, p.y, p.z, p.w};
+            uint32_t w[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {  // what this part leaves
-                const float top = __uint_as_float(i < 4 ? w[i] << 16 : w[i - 4] & 0xffff0000u);
-                v[i] = fabsf(top) <= 3.4e38f ? v[i] - top : 0.f;  // infinities and NaN go with the first part
+            for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(v[i]);
+            dst[4 * j] = make_uint4(__byte_perm(w[0], w[4], 0x7632), __byte_perm(w[1], w[5], 0x7632),
+                                    __byte_perm(w[2], w[6], 0x7632), __byte_perm(w[3], w[7], 0x7632));
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {  // what this part leaves: of an infinity nothing, of a NaN NaN
+                const float top = __uint_as_float(w[i] & 0xffff0000u);
+                v[i] = v[i] == top ? 0.f : v[i] - top;
             }
         }
     } else {

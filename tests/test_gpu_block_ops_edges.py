@@ -105,6 +105,43 @@ def test_rms_norm_least_scale(yt):
     assert ref.within(s[2:], x[2:, 0].double() / top, ref.NORM * x[2:, 0].double() / top) <= 1
 
 
+# ------------------------------------------------------------------------ 4-bit product
+@pytest.mark.parametrize("g", [32, 64, 128])
+@pytest.mark.parametrize("M", [1, 2, 5, 10, 22, 64])
+def test_matvec_w4_products_of_fp32_rows_are_exact(M, g):
+    """Weights that pick one column each (+-1 there, times a power of two): y is x,
+    bit for bit, up to the largest finite value."""
+    K = 2 * g
+    gen = torch.Generator().manual_seed(21)
+    # all 24 bits, exponents from 2^-100 on
+    x = torch.randint(1 << 23, 1 << 24, (M, K), generator=gen).double()
+    x = torch.ldexp(x, torch.randint(-123, 104, (M, K), generator=gen))
+    x[torch.rand(M, K, generator=gen) < 0.5] *= -1
+    x[:, 3], x[:, 4] = torch.finfo(F32).max, -3.395e38
+    x[:, 5] = 0.0
+    x = x.float()
+    sign = torch.where(torch.arange(K) % 3 == 0, -1, 1)
+    q = torch.full((K, K), 8) + torch.diag(sign)
+    wq = (q[:, 0::2] | q[:, 1::2] << 4).to(torch.uint8)
+    for scale in (1.0, 2.0 ** -12):
+        s = torch.full((K, 2), scale, dtype=BF16)
+        y = torch.full((M, K), 7.0, device="cuda")
+        R.ret_matvec_w4(x.cuda(), wq.cuda(), s.cuda(), y)
+        assert torch.equal(y.cpu(), x * sign * scale)
+
+
+def test_matvec_w4_keeps_infinities_and_every_nan():
+    x = torch.ones(4, 64)
+    x[0, 7], x[1, 7] = float("inf"), float("-inf")
+    x[2:, 7] = torch.tensor([0x7f800001, -0x7fffff], dtype=torch.int32).view(F32)   # NaNs with low bits only
+    wq = torch.full((8, 32), 0x99, dtype=torch.uint8)           # weights of 1
+    y = torch.empty(4, 8, device="cuda")
+    R.ret_matvec_w4(x.cuda(), wq.cuda(), torch.ones(8, 1, dtype=BF16).cuda(), y)
+    y = y.cpu()
+    assert bool((y[0] == float("inf")).all()) and bool((y[1] == float("-inf")).all())
+    assert bool(torch.isnan(y[2:]).all())
+
+
 # ------------------------------------------------------------------------ streams
 def busy_then_freed(shapes):
     """Blocks of these (shape, dtype) that the allocator holds for the current
