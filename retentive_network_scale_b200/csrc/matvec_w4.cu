@@ -231,8 +231,8 @@ matvec_w4_kernel(const W4Args a) {
     // staging: this thread's first piece of a chunk, and the way to its next ones
     const int row_first = tid / 4 % nrow, step_first = tid / 4 / nrow;
     const int row_next = (int)blockDim.x / 4 % nrow, step_next = (int)blockDim.x / 4 / nrow;
-    for (int k0 = 0; k0 < a.K; k0 += a.kc) {
-        const int kn = min(a.kc, a.K - k0);
+    for (int left = a.K; left > 0; left -= a.kc) {  // (k0 + a.kc may lie past 2^31)
+        const int k0 = a.K - left, kn = min(a.kc, left);
         if (k0) __syncthreads();
         // x of the chunk: piece (step of 32 columns, product column, c) holds
         // the 8 columns that lane c multiplies in that step

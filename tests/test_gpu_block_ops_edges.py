@@ -142,6 +142,24 @@ def test_matvec_w4_keeps_infinities_and_every_nan():
     assert bool(torch.isnan(y[2:]).all())
 
 
+def test_matvec_w4_with_the_most_columns_an_int_holds():
+    """The last piece of x ends where an int does.  Everything but the first and
+    the last columns is zero."""
+    K, N, g = 2 ** 31 - 128, 2, 128
+    gen = torch.Generator().manual_seed(22)
+    ends = torch.randint(-127, 128, (1, 512), generator=gen, dtype=torch.int8)
+    x = torch.zeros(1, K, device="cuda", dtype=I8)
+    x[:, :256], x[:, -256:] = ends[:, :256].cuda(), ends[:, 256:].cuda()
+    codes = torch.randint(0, 256, (N, 256), generator=gen, dtype=torch.uint8)
+    wq = torch.zeros(N, K // 2, device="cuda", dtype=torch.uint8)
+    wq[:, :128], wq[:, -128:] = codes[:, :128].cuda(), codes[:, 128:].cuda()
+    s = torch.ones(N, K // g, device="cuda", dtype=BF16)
+    y, xs = torch.empty(1, N, device="cuda"), torch.full((1, 1), 0.5, device="cuda")
+    R.ret_matvec_w4(x, wq, s, y, x_scales=xs)
+    want, _ = ref.matvec_w4(ends.float(), codes, torch.ones(N, 4, dtype=BF16))
+    assert torch.equal(y.cpu().double(), want * 0.5)            # whole numbers below 2^24
+
+
 # ------------------------------------------------------------------------ streams
 def busy_then_freed(shapes):
     """Blocks of these (shape, dtype) that the allocator holds for the current
