@@ -537,6 +537,7 @@ ret_status ret_gate_norm_backward(int B, int L, int H, int d_v, int o_dtype,
  * -------------------------------------------------------------------------- */
 
 #define RET_MAX_NORM_WIDTH 16384 /* channels of a ret_rms_norm row           */
+#define RET_MAX_EXTENT 0x7ffffc00 /* L, D of ret_causal_conv, ret_selective_scan */
 #define RET_MAX_CONV_WIDTH 4     /* taps of ret_causal_conv                  */
 #define RET_MAX_SCAN_STATES 128  /* states per channel of ret_selective_scan */
 #define RET_MAX_MATVEC_ROWS 64   /* rows of one ret_matvec_w4                */
@@ -584,7 +585,7 @@ ret_status ret_rms_norm(long long rows, int d, int x_dtype, const void *X,
  *           wanted); state_out may be state_in
  *   Y       device dtype [B][L][D]
  * Single tokens: L = 1 with state_out = state_in.  2 <= width <=
- * RET_MAX_CONV_WIDTH.  Errors: RET_ERR_NULL, _SHAPE, _DTYPE, _ALIGN, _ARG
+ * RET_MAX_CONV_WIDTH; L, D <= RET_MAX_EXTENT.  Errors: RET_ERR_NULL, _SHAPE, _DTYPE, _ALIGN, _ARG
  * (swish), _UNSUPPORTED, _CUDA.
  */
 ret_status ret_causal_conv(int B, int L, int D, int width, int dtype,
@@ -621,7 +622,7 @@ typedef struct {
  *           state_out may be state_in
  *   Y       device dtype [B][L][D]
  * Single tokens: L = 1 with state_out = state_in.  1 <= N <=
- * RET_MAX_SCAN_STATES, G divides D.  Errors: RET_ERR_NULL, _SHAPE, _DTYPE,
+ * RET_MAX_SCAN_STATES, G divides D; L, D <= RET_MAX_EXTENT.  Errors: RET_ERR_NULL, _SHAPE, _DTYPE,
  * _ALIGN, _ARG (softplus), _UNSUPPORTED, _CUDA.
  */
 ret_status ret_selective_scan(const ret_scan_desc *desc, const void *U,

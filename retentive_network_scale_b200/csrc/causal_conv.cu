@@ -233,7 +233,9 @@ extern "C" ret_status ret_causal_conv(int B, int L, int D, int width, int dtype,
                                       const int *lengths, const void *state_in, void *state_out,
                                       void *Y, void *stream) {
     using namespace ret;
-    if (B < 0 || L < 0 || D < 1 || width < 2 || width > RET_MAX_CONV_WIDTH || ldx < D)
+    // (the extents' limit keeps rows and channels rounded up to whole CTAs in an int)
+    if (B < 0 || L < 0 || D < 1 || L > RET_MAX_EXTENT || D > RET_MAX_EXTENT || width < 2 ||
+        width > RET_MAX_CONV_WIDTH || ldx < D)
         return RET_ERR_SHAPE;
     if (dtype != RET_F32 && dtype != RET_BF16) return RET_ERR_DTYPE;
     if (swish != 0 && swish != 1) return RET_ERR_ARG;

@@ -677,8 +677,10 @@ extern "C" ret_status ret_selective_scan(const ret_scan_desc *d, const void *U, 
                                          float *state_out, void *Y, void *stream) {
     using namespace ret;
     if (!d) return RET_ERR_NULL;
-    if (d->B < 0 || d->L < 0 || d->D < 1 || d->N < 1 || d->N > RET_MAX_SCAN_STATES || d->G < 1 ||
-        d->D % d->G)
+    // (the extents' limit keeps rows rounded up to whole tiles of 16 segments, and
+    // channels to whole CTAs, in an int)
+    if (d->B < 0 || d->L < 0 || d->D < 1 || d->L > RET_MAX_EXTENT || d->D > RET_MAX_EXTENT || d->N < 1 ||
+        d->N > RET_MAX_SCAN_STATES || d->G < 1 || d->D % d->G)
         return RET_ERR_SHAPE;
     if (d->dtype != RET_F32 && d->dtype != RET_BF16) return RET_ERR_DTYPE;
     if (d->softplus != 0 && d->softplus != 1) return RET_ERR_ARG;

@@ -44,6 +44,7 @@ RET_STATIC_SCRATCH_FLOATS = 4 << 20
 RET_MAX_DECODE_STEPS = 16
 RET_MAX_SEGMENTS = 64
 RET_MAX_NORM_WIDTH = 16384
+RET_MAX_EXTENT = 0x7ffffc00
 RET_MAX_CONV_WIDTH = 4
 RET_MAX_SCAN_STATES = 128
 RET_MAX_MATVEC_ROWS = 64

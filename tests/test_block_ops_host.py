@@ -150,3 +150,25 @@ def test_block_calls_refuse_what_is_not_a_tensor_of_the_shape(monkeypatch, fn, a
             with pytest.raises(TypeError):
                 fn(**dict(args, **{name: t.to(torch.float64)}))
     assert lib.calls == [fn.__name__]
+
+
+def test_extents_that_would_overflow_an_int_are_refused():
+    """(In every machine's build: refused before any CUDA call.)"""
+    from retentive_network_scale_b200 import build
+    build.build()
+    lib = R.load_library()
+    shape, fake, limit = R.STATUS_NAMES.index("RET_ERR_SHAPE"), 0x10000, R.RET_MAX_EXTENT
+
+    def conv(L, D):
+        return lib.ret_causal_conv(1, L, D, 4, R.RET_BF16, fake, D, fake, None, 1, None, None, None, fake, None)
+
+    def scan(L, D):
+        d = R.RetScanDesc(1, L, D, 4, 1, R.RET_BF16, 1, D, D, D, 4, 4)
+        return lib.ret_selective_scan(d, fake, fake, None, fake, fake, fake, None, None, None, None, None, fake, None)
+
+    for call in (conv, scan):
+        for big in (limit + 1, 2 ** 31 - 127, 2 ** 31 - 1):
+            assert call(big, 1) == shape and call(1, big) == shape
+    if not torch.cuda.is_available():           # valid but for the machine
+        unsupported = R.STATUS_NAMES.index("RET_ERR_UNSUPPORTED")
+        assert conv(limit, 1) == conv(1, limit) == scan(limit, 1) == scan(1, limit) == unsupported

@@ -105,6 +105,41 @@ def test_rms_norm_least_scale(yt):
     assert ref.within(s[2:], x[2:, 0].double() / top, ref.NORM * x[2:, 0].double() / top) <= 1
 
 
+# ------------------------------------------------------------------------ convolution, scan
+def test_conv_and_scan_of_the_most_rows():
+    """One channel; its last rows are checked (of the scan, which would take tens of
+    seconds, a short sequence in a padded batch of that many rows)."""
+    L = R.RET_MAX_EXTENT
+    x = torch.zeros(1, L, 1, device="cuda", dtype=BF16)
+    tail, w = rt((1, 300, 1), 31, 1.0, BF16), rt((1, 2), 32)
+    x[:, -300:] = tail.cuda()
+    x[:, :300] = tail.cuda()
+    y, end = torch.zeros_like(x), torch.empty(1, 1, 1, device="cuda", dtype=BF16)
+    R.ret_causal_conv(x, w.cuda(), y, state_out=end)
+    want, last, tol = ref.causal_conv(tail, w)
+    assert ref.within(y[:, -300:], want, tol + ref.rounded(want, BF16)) <= 1
+    assert torch.equal(end.cpu().double(), last)
+    y.fill_(5.0)
+    A, n = torch.full((1, 1), -0.5), torch.tensor([300], dtype=torch.int32)
+    R.ret_selective_scan(x, x, A.cuda(), x, x, y, lengths=n.cuda())
+    tail4 = tail[..., None]
+    want, _, tol, _ = ref.selective_scan(tail, tail, A, tail4, tail4)
+    assert ref.within(y[:, :300], want, tol + ref.rounded(want, BF16)) <= 1
+    assert bool((y[0, 300:1000] == 5.0).all()) and bool((y[0, -1000:] == 5.0).all())
+
+
+def test_conv_of_the_most_channels_a_call_takes():
+    """Rows so wide that the last threads' channels lie past 2^31 unless cut."""
+    D = R.RET_MAX_EXTENT - 2                    # two channels a thread
+    x = torch.zeros(1, 1, D, device="cuda", dtype=BF16)
+    x[0, 0, -256:] = rt((256,), 33, 1.0, BF16).cuda()
+    w = torch.zeros(D, 2, device="cuda")
+    w[:, 1] = 2.0
+    y = torch.full_like(x, 5.0)
+    R.ret_causal_conv(x, w, y, swish=False)
+    assert torch.equal(y[0, 0, -256:], 2 * x[0, 0, -256:]) and bool((y[0, 0, :4096] == 0).all())
+
+
 # ------------------------------------------------------------------------ 4-bit product
 @pytest.mark.parametrize("g", [32, 64, 128])
 @pytest.mark.parametrize("M", [1, 2, 5, 10, 22, 64])
