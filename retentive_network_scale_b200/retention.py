@@ -702,6 +702,13 @@ def _tensor(t, name, *dims):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {' or '.join(map(str, dims))} dimensions")
 
 
+def _ints(*sizes):
+    """Raises for a size that the C interface's int does not hold (ctypes would cut
+    it off without a word)."""
+    if max(sizes) > 0x7fffffff:
+        raise ValueError(f"a size of {max(sizes)} is past 2^31 - 1")
+
+
 def _on(t, name, shape, dtype, device):
     """Address of a dense tensor of the call's device (None: none)."""
     if t is None:
@@ -766,6 +773,7 @@ def ret_rms_norm(X, Y, weight=None, residual=None, residual_out=None, scales=Non
     dims = len(shape)
     _tensor(Y, "Y", dims)
     d = shape[-1]
+    _ints(d)
     px, ldx = _rows(X, "X", shape, X.dtype, device)
     rows = X.numel() // d if d else 0
     y_dtype = _CODES.get(Y.dtype)
@@ -812,6 +820,7 @@ def ret_causal_conv(X, weight, Y, bias=None, swish=True, lengths=None, state_in=
     _tensor(weight, "weight", 2)
     B, L, D = X.shape
     width = weight.shape[-1]
+    _ints(B, L, D, width)
     dt = X.dtype
     px, ldx = _rows(X, "X", X.shape, dt, device)
     held = (B, width - 1, D)
@@ -843,6 +852,7 @@ def ret_selective_scan(U, delta, A, Bm, Cm, Y, skip=None, Z=None, delta_bias=Non
     else:
         G = Bm.shape[2]
         gn = (B, L, G, N)
+    _ints(B, L, D, N, G)
     pu, ldu = _rows(U, "U", shape, dt, device)
     pd, ldd = _rows(delta, "delta", shape, dt, device)
     pz, ldz = (None, 0) if Z is None else _rows(Z, "Z", shape, dt, device)
@@ -872,6 +882,7 @@ def ret_matvec_w4(X, Wq, scales, Y, zeros=None, x_scales=None, stream=None):
     _tensor(Y, "Y", 2)
     M, K = X.shape
     N, groups = scales.shape
+    _ints(M, K, N)
     x_dtype = _CODES.get(X.dtype)
     if x_dtype is None:
         raise TypeError(f"unsupported dtype {X.dtype}")
@@ -906,6 +917,7 @@ def ret_quantize_w4(W, group, zeros=False, stream=None):
     device = _device_of(W, "W")
     _tensor(W, "W", 2)
     K, N = W.shape
+    _ints(K, N, group)
     pw, ldw = _rows(W, "W", W.shape, W.dtype, device)
     wq = _empty((N, K // 2), torch.uint8, W.device, stream)
     groups = K // group if group > 0 else 0

@@ -172,3 +172,24 @@ def test_extents_that_would_overflow_an_int_are_refused():
     if not torch.cuda.is_available():           # valid but for the machine
         unsupported = R.STATUS_NAMES.index("RET_ERR_UNSUPPORTED")
         assert conv(limit, 1) == conv(1, limit) == scan(limit, 1) == scan(1, limit) == unsupported
+
+
+def test_sizes_past_an_int_are_refused_by_the_binding(monkeypatch):
+    """2^32 + 64 would arrive in the library as 64."""
+    lib = FakeLibrary()
+    monkeypatch.setattr(R, "load_library", lambda *a: lib)
+    monkeypatch.setattr(R, "_device_of", lambda t, name: -1)
+    monkeypatch.setattr(R, "_on_stream", lambda stream, device: 0)
+    big = 2 ** 32 + 64
+    e = lambda *shape, dtype=torch.float32: torch.empty(*shape, device="meta", dtype=dtype)  # noqa: E731
+    u8, bf = torch.uint8, torch.bfloat16
+    for call in (lambda: R.ret_rms_norm(e(2, big), e(2, big)),
+                 lambda: R.ret_causal_conv(e(1, big, 1), e(1, 4), e(1, big, 1)),
+                 lambda: R.ret_causal_conv(e(1, 1, big), e(big, 4), e(1, 1, big)),
+                 lambda: R.ret_selective_scan(*[e(1, big, 1)] * 2, e(1, 1), *[e(1, big, 1)] * 3),
+                 lambda: R.ret_matvec_w4(e(1, big), e(1, big // 2, dtype=u8), e(1, big // 64, dtype=bf), e(1, 1)),
+                 lambda: R.ret_matvec_w4(e(1, 64), e(big, 32, dtype=u8), e(big, 1, dtype=bf), e(1, big)),
+                 lambda: R.ret_quantize_w4(e(64, 8), big)):
+        with pytest.raises(ValueError, match="2\\^31"):
+            call()
+    assert lib.calls == []
