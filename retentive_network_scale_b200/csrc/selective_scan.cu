@@ -414,25 +414,35 @@ selective_scan_kernel(const ScanArgs a) {
         for (int j = 0; j < PR; ++j) {
             const uint64_t p = tc::f2_mul(dup(sum_d), A2[j]);
             const int n = state_of(2 * j);
-            // (a decay past the largest float would make NaN of a zero state)
-            *reinterpret_cast<float2 *>(&seg.a[ch][n]) =
-                make_float2(fminf(exp2_fast(tc::f2_lo(p)), 3.4e38f), fminf(exp2_fast(tc::f2_hi(p)), 3.4e38f));
+            // (a growth past fp32's range is passed on as its exponent, negated)
+            auto factor = [](float e) { return e <= 127.f ? exp2_fast(e) : -e; };
+            *reinterpret_cast<float2 *>(&seg.a[ch][n]) = make_float2(factor(tc::f2_lo(p)), factor(tc::f2_hi(p)));
             *reinterpret_cast<uint64_t *>(&seg.b[ch][n]) = h[j];
         }
         __syncthreads();
         if (first < end) copy_tile(first, 0, true);
         tc::cluster_sync();
-        // 2. the state that enters this segment, through those before it
+        // 2. the state that enters this segment, through those before it (a growth
+        //    2^-a in three factors: a small or zero state stays what it is)
+        auto grow = [](float &a, float v) {
+            if (a < 0.f) {
+                v *= exp2_fast(fminf(-a - 127.f, 127.f));
+                v *= exp2_fast(fminf(fmaxf(-a - 254.f, 0.f), 127.f));
+                a = 0x1p127f;
+            }
+            return v;
+        };
 #pragma unroll
         for (int j = 0; j < PR; ++j) {
             const uint32_t at_a = (uint32_t)__cvta_generic_to_shared(&seg.a[ch][state_of(2 * j)]);
             const uint32_t at_b = (uint32_t)__cvta_generic_to_shared(&seg.b[ch][state_of(2 * j)]);
             h[j] = me == 0 ? entering(j) : 0;
             for (int i = 0; i < me; ++i) {
-                const float2 ai = tc::ld_cluster_f32x2(tc::map_to_rank(at_a, i));
+                float2 ai = tc::ld_cluster_f32x2(tc::map_to_rank(at_a, i));
                 const float2 bi = tc::ld_cluster_f32x2(tc::map_to_rank(at_b, i));
                 const uint64_t b2 = tc::f2_make(bi.x, bi.y);
-                h[j] = i ? tc::f2_fma(tc::f2_make(ai.x, ai.y), h[j], b2) : b2;
+                const uint64_t in = i ? tc::f2_make(grow(ai.x, tc::f2_lo(h[j])), grow(ai.y, tc::f2_hi(h[j]))) : 0;
+                h[j] = i ? tc::f2_fma(tc::f2_make(ai.x, ai.y), in, b2) : b2;
             }
         }
         tc::cluster_sync();  // nothing of this CTA's is read after this; state_out may be state_in

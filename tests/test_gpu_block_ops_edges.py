@@ -1,6 +1,8 @@
 """The operators around the mixers on the GPU at the ends of their ranges: tiny and
 non-finite rows, layouts and lengths that take every form of each kernel, streams
 that are not the current one.  References and bounds as in block_ref."""
+import math
+
 import pytest
 import torch
 
@@ -106,6 +108,38 @@ def test_rms_norm_least_scale(yt):
 
 
 # ------------------------------------------------------------------------ convolution, scan
+def test_scan_segment_that_grows_past_fp32():
+    """One segment multiplies the state by 2^140 to 2^270 (which fp32 does not
+    hold), the state itself staying inside fp32; a zero state stays zero."""
+    B, L, D, N = 1, 1100, 8, 16
+    for grown, s0 in ((140.0, 2.0 ** -60), (200.0, -2.0 ** -100), (270.0, 2.0 ** -145), (140.0, 0.0)):
+        u = torch.zeros(B, L, D)
+        delta = torch.zeros(B, L, D)
+        # all growth in the second of the 16 segments of 80 rows
+        delta[:, 80:160] = grown / 80 * 0.6931471805599453 / 0.25
+        A = torch.full((D, N), 0.25)
+        bm, cm = torch.ones(B, L, 1, N), torch.ones(B, L, 1, N)
+        state = torch.full((B, D, N), s0)
+        y, out = torch.empty(B, L, D, device="cuda"), torch.empty(B, D, N, device="cuda")
+        R.ret_selective_scan(u.cuda(), delta.cuda(), A.cuda(), bm.cuda(), cm.cuda(), y, softplus=False,
+                             state_in=state.cuda(), state_out=out)
+        want, last, tol, stol = ref.selective_scan(u, delta, A, bm, cm, softplus=False, state=state)
+        # The bound counts roundings of normal numbers.  A subnormal state is rounded
+        # to 2^-149 in every row, off by up to 2^-150, which the rows after it grow:
+        # E_t = a_t E_{t-1} + 2^-150 more (2^-145 grown 2^3.4 a row ends up 3% off).
+        E, sub = 0.0, torch.zeros(1, L, 1, dtype=torch.float64)
+        for t in range(L):
+            E = math.exp(float(delta[0, t, 0]) * 0.25) * E + (2.0 ** -150 if s0 else 0.0)
+            sub[0, t] = E
+        assert ref.within(out, last, stol + E) <= 1
+        tol = tol + N * sub
+        # (16 states of 2^125 add up to more than fp32 holds: the y that belongs there)
+        past = want.abs() > torch.finfo(F32).max
+        assert bool((y.cpu()[past] == want[past].sign().float() * float("inf")).all())
+        got, want = torch.where(past, 0.0, y.cpu().double()), torch.where(past, 0.0, want)
+        assert ref.within(got, want, tol + ref.rounded(want, F32) + 2.0 ** -149) <= 1
+
+
 def test_conv_and_scan_of_the_most_rows():
     """One channel; its last rows are checked (of the scan, which would take tens of
     seconds, a short sequence in a padded batch of that many rows)."""
