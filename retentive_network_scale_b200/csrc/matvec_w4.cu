@@ -419,16 +419,22 @@ __global__ void quantize_w4_kernel(int K, int N, int group, const T *W, long lon
         lo = fminf(lo, v);
         hi = fmaxf(hi, v);
     }
-    // with zero points [lo, hi] (0 included) to 0..15, else +-max to 8 +- 7
-    const __nv_bfloat16 sb = __float2bfloat16_rn(zeros ? (hi - lo) / 15.f : fmaxf(hi, -lo) / 7.f);
-    const float s = __bfloat162float(sb), inv = s > 0.f ? 1.f / s : 0.f;
-    const float z = zeros ? fminf(fmaxf(rintf(-lo * inv), 0.f), 15.f) : 8.f;
+    // with zero points [lo, hi] (0 included) to 0..15, else +-max to 8 +- 7 (halves:
+    // hi - lo may pass the largest float)
+    const __nv_bfloat16 sb = __float2bfloat16_rn(zeros ? (0.5f * hi - 0.5f * lo) / 7.5f : fmaxf(hi, -lo) / 7.f);
+    const float s = __bfloat162float(sb);
+    // steps of the scale, to the nearest, exactly: w / s next to k + 1/2 cannot round
+    // onto it (s (k + 1/2) has 13 bits, so is itself an fp32 number, and the ones beside
+    // it are farther off than a quotient's rounding); 1 / s, which would be quicker to
+    // multiply by, decides ties either way and is infinite for subnormal scales
+    auto steps = [s](float w) { return s > 0.f ? rintf(w / s) : 0.f; };
+    const float z = zeros ? fminf(fmaxf(steps(-lo), 0.f), 15.f) : 8.f;
     scales[(long long)n * groups + g] = sb;
     if (zeros) zeros[(long long)n * groups + g] = (uint8_t)z;
     uint8_t *p = wq + (long long)n * (K / 2) + (long long)g * (group / 2);
     for (int k = 0; k < group; k += 2) {
-        const float a = fminf(fmaxf(rintf(ld(w, (size_t)k * ldw) * inv) + z, 0.f), 15.f);
-        const float b = fminf(fmaxf(rintf(ld(w, (size_t)(k + 1) * ldw) * inv) + z, 0.f), 15.f);
+        const float a = fminf(fmaxf(steps(ld(w, (size_t)k * ldw)) + z, 0.f), 15.f);
+        const float b = fminf(fmaxf(steps(ld(w, (size_t)(k + 1) * ldw)) + z, 0.f), 15.f);
         p[k / 2] = (uint8_t)((uint32_t)a | (uint32_t)b << 4);
     }
 }

@@ -229,6 +229,47 @@ def test_matvec_w4_with_the_most_columns_an_int_holds():
     assert torch.equal(y.cpu().double(), want * 0.5)            # whole numbers below 2^24
 
 
+def check_quantized(W, g, zeros):
+    """Scales as the definition's (in fp32, rounded to bf16), codes and zero points
+    exactly the nearest, ties to even, for those scales."""
+    K, N = W.shape
+    wq, s, z = (t if t is None else t.cpu() for t in R.ret_quantize_w4(W.cuda(), g, zeros=zeros))
+    t = W.double().view(K // g, g, N)
+    lo, hi = t.amin(1).clamp(max=0), t.amax(1).clamp(min=0)
+    # (the range is rounded to fp32 before its division, as halves)
+    scale = ((hi - lo) / 2).float() / 7.5 if zeros else torch.maximum(hi, -lo).float() / 7
+    assert torch.equal(s, scale.to(BF16).t())
+    d = s.double().t()
+    per = lambda v: torch.where(d > 0, v / torch.where(d > 0, d, 1.0), 0.0).round()  # noqa: E731
+    zp = per(-lo).clamp(0, 15) if zeros else torch.full_like(lo, 8.0)
+    if zeros:
+        assert torch.equal(z.double().t(), zp)
+    steps = torch.where(d[:, None] > 0, t / torch.where(d > 0, d, 1.0)[:, None], 0.0).round()
+    want = (steps + zp[:, None]).clamp(0, 15).view(K, N).t()
+    got = torch.stack([wq & 15, wq >> 4], -1).view(N, K).double()
+    assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("wt", [F32, BF16])
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("size", [1.0, 1e-37, 3e-39, 1e-40, 1e37, 8e37])
+def test_quantize_w4_rounds_to_the_nearest_at_every_size(wt, zeros, size):
+    K, N, g = 256, 96, 64
+    W = (rt((K, N), 41).clamp(-4, 4) * size).to(wt)
+    W[::7] = 0.0
+    W[:g, 5] = 0.0
+    check_quantized(W, g, zeros)
+
+
+def test_quantize_w4_ties_go_to_even():
+    """w = (k + 1/2) scale, for every mantissa of a bf16 scale."""
+    scale = torch.arange(128, 256).float() / 1024                       # one column each
+    steps = torch.cat([torch.tensor([7.0]), torch.arange(-7, 7) + 0.5, torch.zeros(17)])
+    check_quantized(steps[:, None] * scale[None], 32, False)
+    steps = torch.cat([torch.tensor([8.0, -7.0]), torch.arange(-7, 8) + 0.5, torch.zeros(15)])
+    check_quantized(steps[:, None] * scale[None], 32, True)
+
+
 # ------------------------------------------------------------------------ streams
 def busy_then_freed(shapes):
     """Blocks of these (shape, dtype) that the allocator holds for the current
