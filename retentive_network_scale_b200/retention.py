@@ -694,35 +694,44 @@ def _refuse(t, name, shape, dtype, device):
     raise ValueError(f"{name} must be contiguous")
 
 
-def _tensor(t, name, *dims):
-    """Raises unless t is a tensor of one of these numbers of dimensions."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dim() not in dims:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {' or '.join(map(str, dims))} dimensions")
+def _refuse_ranks(**expected):
+    """Raises for the first of name=(tensor, numbers of dimensions..) that is not one;
+    for the calls to find out by what they could not take a tensor apart."""
+    for name, (t, *dims) in expected.items():
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a CUDA tensor")
+        if t.dim() not in dims:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {' or '.join(map(str, dims))} dimensions")
 
 
-def _ints(*sizes):
-    """Raises for a size that the C interface's int does not hold (ctypes would cut
-    it off without a word)."""
-    if max(sizes) > 0x7fffffff:
-        raise ValueError(f"a size of {max(sizes)} is past 2^31 - 1")
+_INT_MAX = 0x7fffffff  # (ctypes would cut a larger size off without a word)
+
+
+def _refuse_sizes(*sizes):
+    raise ValueError(f"a size of {max(sizes)} is past 2^31 - 1")
 
 
 def _on(t, name, shape, dtype, device):
     """Address of a dense tensor of the call's device (None: none)."""
     if t is None:
         return None
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape or t.get_device() != device or not t.is_contiguous():
-        _refuse(t, name, shape, dtype, device)
-    return t.data_ptr()
+    try:
+        if t.dtype == dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(t, name, shape, dtype, device)
 
 
 def _rows(t, name, shape, dtype, device):
     """Address and leading dimension of strided rows: unit stride along the
     last dimension (or, of [B, L, G, N], dense in the last two), one stride between
     all rows before it."""
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape or t.get_device() != device:
+    try:
+        fits = t.dtype == dtype and t.shape == shape and t.get_device() == device
+    except AttributeError:
+        fits = False
+    if not fits:
         _refuse(t, name, shape, dtype, device)
     stride, n = t.stride(), shape[-1]
     if len(shape) == 4:
@@ -768,23 +777,29 @@ def ret_rms_norm(X, Y, weight=None, residual=None, residual_out=None, scales=Non
     scales [.., groups] (fp32): one per row, or per 32, 64 or 128 channels.
     Returns Y."""
     device = _device_of(X, "X")
-    _tensor(X, "X", 2, 3)
     shape = X.shape
-    dims = len(shape)
-    _tensor(Y, "Y", dims)
+    if not 2 <= len(shape) <= 3:
+        raise ValueError("X must have rows [M, d] or [B, L, d]")
+    try:
+        y_dtype = _CODES.get(Y.dtype)
+        groups = scales.shape[-1] if scales is not None else 0
+        r_torch = residual.dtype if residual is not None else None
+    except (AttributeError, IndexError):
+        dims = len(shape)
+        _refuse_ranks(Y=(Y, dims), **{n: (t, dims) for n, t in (("scales", scales), ("residual", residual))
+                                      if t is not None})
+        raise
     d = shape[-1]
-    _ints(d)
+    if d > _INT_MAX:
+        _refuse_sizes(d)
     px, ldx = _rows(X, "X", shape, X.dtype, device)
     rows = X.numel() // d if d else 0
-    y_dtype = _CODES.get(Y.dtype)
     if y_dtype is None or X.dtype not in (torch.float32, torch.bfloat16):
         raise TypeError(f"unsupported dtypes {X.dtype} -> {Y.dtype}")
     group, r_dtype = 0, RET_F32
     if y_dtype >= RET_I8:
         if scales is None:
             raise ValueError("an 8-bit Y needs scales")
-        _tensor(scales, "scales", dims)
-        groups = scales.shape[-1]
         if groups < 1 or d % groups:
             raise ValueError("scales must divide the channels into equal groups")
         group = 0 if groups == 1 else d // groups
@@ -794,15 +809,13 @@ def ret_rms_norm(X, Y, weight=None, residual=None, residual_out=None, scales=Non
     else:
         ps = None
     if residual is not None:
-        _tensor(residual, "residual", dims)
         r_dtype = _dtype_code(residual)
     elif residual_out is not None:
         raise ValueError("residual_out needs residual")
     _check(load_library().ret_rms_norm(
         rows, d, _dtype_code(X), px, ldx, _on(weight, "weight", (d,), torch.float32, device), r_dtype,
-        _on(residual, "residual", shape, residual.dtype if residual is not None else None, device),
-        _on(residual_out, "residual_out", shape, residual.dtype if residual is not None else None,
-            device),
+        _on(residual, "residual", shape, r_torch, device),
+        _on(residual_out, "residual_out", shape, r_torch, device),
         eps, y_dtype, _on(Y, "Y", shape, Y.dtype, device), group, ps, _on_stream(stream, device)),
         "ret_rms_norm")
     return Y
@@ -816,11 +829,14 @@ def ret_causal_conv(X, weight, Y, bias=None, swish=True, lengths=None, state_in=
     both updates it in place; L = 1 is a single token), lengths [B] (int32) the
     valid rows of a padded batch.  Returns (Y, state_out)."""
     device = _device_of(X, "X")
-    _tensor(X, "X", 3)
-    _tensor(weight, "weight", 2)
-    B, L, D = X.shape
-    width = weight.shape[-1]
-    _ints(B, L, D, width)
+    try:
+        B, L, D = X.shape
+        width = weight.shape[-1]
+    except (AttributeError, IndexError, ValueError):
+        _refuse_ranks(X=(X, 3), weight=(weight, 2))
+        raise
+    if B > _INT_MAX or L > _INT_MAX or D > _INT_MAX or width > _INT_MAX:
+        _refuse_sizes(B, L, D, width)
     dt = X.dtype
     px, ldx = _rows(X, "X", X.shape, dt, device)
     held = (B, width - 1, D)
@@ -841,18 +857,20 @@ def ret_selective_scan(U, delta, A, Bm, Cm, Y, skip=None, Z=None, delta_bias=Non
     L = 1 is a single token), lengths [B] (int32) the valid rows of a padded
     batch.  Returns (Y, state_out)."""
     device = _device_of(U, "U")
-    _tensor(U, "U", 3)
-    _tensor(A, "A", 2)
-    _tensor(Bm, "Bm", 3, 4)
-    shape, dt = U.shape, U.dtype
-    B, L, D = shape
-    N = A.shape[-1]
-    if Bm.dim() == 3:
-        G, gn = 1, (B, L, N)
-    else:
-        G = Bm.shape[2]
-        gn = (B, L, G, N)
-    _ints(B, L, D, N, G)
+    try:
+        shape, dt = U.shape, U.dtype
+        B, L, D = shape
+        N = A.shape[-1]
+        if Bm.dim() == 3:
+            G, gn = 1, (B, L, N)
+        else:
+            G = Bm.shape[2]
+            gn = (B, L, G, N)
+    except (AttributeError, IndexError, TypeError, ValueError):
+        _refuse_ranks(U=(U, 3), A=(A, 2), Bm=(Bm, 3, 4))
+        raise
+    if B > _INT_MAX or L > _INT_MAX or D > _INT_MAX or N > _INT_MAX or G > _INT_MAX:
+        _refuse_sizes(B, L, D, N, G)
     pu, ldu = _rows(U, "U", shape, dt, device)
     pd, ldd = _rows(delta, "delta", shape, dt, device)
     pz, ldz = (None, 0) if Z is None else _rows(Z, "Z", shape, dt, device)
@@ -877,12 +895,17 @@ def ret_matvec_w4(X, Wq, scales, Y, zeros=None, x_scales=None, stream=None):
     [N,K/2] (uint8) with scales [N,K/group] (bfloat16) and zeros (uint8, same
     shape).  Returns Y."""
     device = _device_of(X, "X")
-    _tensor(X, "X", 2)
-    _tensor(scales, "scales", 2)
-    _tensor(Y, "Y", 2)
-    M, K = X.shape
-    N, groups = scales.shape
-    _ints(M, K, N)
+    try:
+        M, K = X.shape
+        N, groups = scales.shape
+        y_torch = Y.dtype
+        xgs = x_scales.shape[-1] if x_scales is not None else 0
+    except (AttributeError, IndexError, ValueError):
+        _refuse_ranks(X=(X, 2), scales=(scales, 2), Y=(Y, 2),
+                      **(dict(x_scales=(x_scales, 2)) if x_scales is not None else {}))
+        raise
+    if M > _INT_MAX or K > _INT_MAX or N > _INT_MAX:
+        _refuse_sizes(M, K, N)
     x_dtype = _CODES.get(X.dtype)
     if x_dtype is None:
         raise TypeError(f"unsupported dtype {X.dtype}")
@@ -893,12 +916,10 @@ def ret_matvec_w4(X, Wq, scales, Y, zeros=None, x_scales=None, stream=None):
     if x_dtype >= RET_I8:
         if x_scales is None:
             raise ValueError("8-bit rows need x_scales")
-        _tensor(x_scales, "x_scales", 2)
-        n = x_scales.shape[-1]
-        if n < 1 or K % n:
+        if xgs < 1 or K % xgs:
             raise ValueError("x_scales must divide the columns into equal groups")
-        x_group = 0 if n == 1 else K // n
-        xg = _on(x_scales, "x_scales", (M, n), torch.float32, device)
+        x_group = 0 if xgs == 1 else K // xgs
+        xg = _on(x_scales, "x_scales", (M, xgs), torch.float32, device)
     elif x_scales is not None:
         raise ValueError("x_scales go with 8-bit rows")
     _check(load_library().ret_matvec_w4(
@@ -906,7 +927,7 @@ def ret_matvec_w4(X, Wq, scales, Y, zeros=None, x_scales=None, stream=None):
         _on(Wq, "Wq", (N, K // 2), torch.uint8, device),
         _on(scales, "scales", (N, groups), torch.bfloat16, device),
         _on(zeros, "zeros", (N, groups), torch.uint8, device), _dtype_code(Y),
-        _on(Y, "Y", (M, N), Y.dtype, device), _on_stream(stream, device)), "ret_matvec_w4")
+        _on(Y, "Y", (M, N), y_torch, device), _on_stream(stream, device)), "ret_matvec_w4")
     return Y
 
 
@@ -915,9 +936,9 @@ def ret_quantize_w4(W, group, zeros=False, stream=None):
     with `zeros`, a zero point) per `group` rows of each column.  Returns
     (Wq [N,K/2] uint8, scales [N,K/group] bfloat16, zeros uint8 or None)."""
     device = _device_of(W, "W")
-    _tensor(W, "W", 2)
     K, N = W.shape
-    _ints(K, N, group)
+    if K > _INT_MAX or N > _INT_MAX or group > _INT_MAX:
+        _refuse_sizes(K, N, group)
     pw, ldw = _rows(W, "W", W.shape, W.dtype, device)
     wq = _empty((N, K // 2), torch.uint8, W.device, stream)
     groups = K // group if group > 0 else 0
