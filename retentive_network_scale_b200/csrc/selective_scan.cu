@@ -422,29 +422,38 @@ selective_scan_kernel(const ScanArgs a) {
         __syncthreads();
         if (first < end) copy_tile(first, 0, true);
         tc::cluster_sync();
-        // 2. the state that enters this segment, through those before it (a growth
-        //    2^-a in three factors: a small or zero state stays what it is)
-        auto grow = [](float &a, float v) {
-            if (a < 0.f) {
-                v *= exp2_fast(fminf(-a - 127.f, 127.f));
-                v *= exp2_fast(fminf(fmaxf(-a - 254.f, 0.f), 127.f));
-                a = 0x1p127f;
-            }
-            return v;
-        };
+        // 2. the state that enters this segment, through those before it
+        auto join = [&](auto apply) {
 #pragma unroll
-        for (int j = 0; j < PR; ++j) {
-            const uint32_t at_a = (uint32_t)__cvta_generic_to_shared(&seg.a[ch][state_of(2 * j)]);
-            const uint32_t at_b = (uint32_t)__cvta_generic_to_shared(&seg.b[ch][state_of(2 * j)]);
-            h[j] = me == 0 ? entering(j) : 0;
-            for (int i = 0; i < me; ++i) {
-                float2 ai = tc::ld_cluster_f32x2(tc::map_to_rank(at_a, i));
-                const float2 bi = tc::ld_cluster_f32x2(tc::map_to_rank(at_b, i));
-                const uint64_t b2 = tc::f2_make(bi.x, bi.y);
-                const uint64_t in = i ? tc::f2_make(grow(ai.x, tc::f2_lo(h[j])), grow(ai.y, tc::f2_hi(h[j]))) : 0;
-                h[j] = i ? tc::f2_fma(tc::f2_make(ai.x, ai.y), in, b2) : b2;
+            for (int j = 0; j < PR; ++j) {
+                const uint32_t at_a = (uint32_t)__cvta_generic_to_shared(&seg.a[ch][state_of(2 * j)]);
+                const uint32_t at_b = (uint32_t)__cvta_generic_to_shared(&seg.b[ch][state_of(2 * j)]);
+                h[j] = me == 0 ? entering(j) : 0;
+                for (int i = 0; i < me; ++i) {
+                    const float2 ai = tc::ld_cluster_f32x2(tc::map_to_rank(at_a, i));
+                    const float2 bi = tc::ld_cluster_f32x2(tc::map_to_rank(at_b, i));
+                    const uint64_t b2 = tc::f2_make(bi.x, bi.y);
+                    h[j] = i ? apply(ai, h[j], b2) : b2;
+                }
             }
-        }
+        };
+        float least = 0.f;
+        join([&](float2 a, uint64_t v, uint64_t b) {
+            least = fminf(least, fminf(a.x, a.y));
+            return tc::f2_fma(tc::f2_make(a.x, a.y), v, b);
+        });
+        if (least < 0.f)  // a growth 2^-a, in three factors: a small or zero state stays what it is
+            join([&](float2 a, uint64_t v, uint64_t b) {
+                auto grow = [](float &f, float x) {
+                    if (!(f < 0.f)) return x;
+                    x *= exp2_fast(fminf(-f - 127.f, 127.f));
+                    x *= exp2_fast(fminf(fmaxf(-f - 254.f, 0.f), 127.f));
+                    f = 0x1p127f;
+                    return x;
+                };
+                const float lo = grow(a.x, tc::f2_lo(v)), hi = grow(a.y, tc::f2_hi(v));
+                return tc::f2_fma(tc::f2_make(a.x, a.y), tc::f2_make(lo, hi), b);
+            });
         tc::cluster_sync();  // nothing of this CTA's is read after this; state_out may be state_in
     }
     run(std::true_type{});
