@@ -3,8 +3,8 @@
 //     h_t = exp(d_t A) h_{t-1} + d_t u_t B_t,  y_t = (C_t . h_t + skip u_t) swish(z_t),
 // per channel with N states, for prompts and for single tokens over an fp32
 // state.
+#include <algorithm>
 #include <cmath>
-#include <type_traits>
 #include <type_traits>
 
 #include "common.cuh"
@@ -616,14 +616,35 @@ cudaError_t launch_tokens(const ScanArgs &a, cudaStream_t st) {
     return launch_token_t<T, 4>(a, 8, st);
 }
 
-// Segments a sequence is cut into.  One warp per scheduler alone takes about 170
-// cycles a row and each further one 81 more (8 x 4096 x 4096 against 1 x 16384 x
-// 1024), and a cut sequence runs its rows about 1.8 times.
-int segments_of(long long warps, int L, int tile) {
-    const long long schedulers = 148 * 4;
+// Segments that a sequence of L rows is cut into, 1, 4, 8 or 16, by the time that
+// each would take, in us.  An SM with one CTA takes `row` for a row; with w CTAs an
+// uncut sequence takes 0.38 + 0.53 w of that and a cut one, whose rows run about
+// twice, 0.8 + w, where w is what the fullest SM has (at most per_sm at a time;
+// clusters of 8 and 16 fill the SMs 10% less evenly).  Joining costs a few us, and
+// most for many clusters of 16.
+//
+// Measured, us, uncut / 4 / 8 / 16 segments, 2048 rows (8192), bf16 if not said, by the
+// CTAs of uncut sequences; * is chosen here.  Over 180 shapes (8 to 128 states, fp32 and
+// bf16, 4 to 512 CTAs, 512 to 8192 rows) the choice is 0.7% off the best on average,
+// 15% at worst; one made from the warps alone, whatever the layout, was 12% and 126% off.
+//   16 states,  16 CTAs   173 /  83 /  62 /  56*      (685 /  317 /  227 /  162*)
+//               32 CTAs   176 /  86 /  67*/  90       (689 /  318 /  236 /  259*)
+//               64 CTAs   176 / 120 / 113*/ 147       (689 /  461 /  427*/  430)
+//       fp32    64 CTAs   180 / 125*/ 137 / 181       (705 /  480 /  498 /  514*)
+//              128 CTAs   176*/ 212 / 200 / 261       (689*/  826 /  756 /  790)
+//    8 states, 128 CTAs   145*/ 130 / 131 / 162       (566*/  504 /  494 /  505)
+//   64 states,  32 CTAs   170 /  77 /  62*/  83       (674 /  291 /  229 /  249*)
+//  128 states,  32 CTAs   276 / 127 / 112*/ 182      (1097 /  479 /  424*/  513)
+//              128 CTAs   278*/ 385 / 410 / 627
+int segments_of(long long ctas, size_t smem, int spt, int L, int tile) {
+    const double row = spt == 4 ? 0.065 : spt == 8 ? 0.084 : 0.135;
+    const int per_sm = std::min<int>(spt <= 8 ? 4 : 3, 227 * 1024 / (int)(smem + 1024));
     auto cost = [&](int s) {
-        const double w = (double)((warps * s + schedulers - 1) / schedulers);
-        return (s > 1 ? 1.8 : 1.0) / s * (90.0 + 81.0 * w);
+        const double w = (double)(ctas * s) / 148, even = s > 4 ? 1.1 * w : w;
+        const double rounds = std::floor(even / per_sm), rest = std::ceil(even - rounds * per_sm - 1e-9);
+        auto rows = [s](double v) { return s == 1 ? std::max(1.0, 0.38 + 0.53 * v) : 0.8 + v; };
+        const double t = rounds * rows(per_sm) + (rest > 0 ? rows(rest) : 0.0);
+        return L * row * t / s + (s == 1 ? 0.0 : s == 4 ? 4 + w : s == 8 ? 4.5 + w : 3 + 5 * w);
     };
     int best = 1;
     for (int s = 4; s <= 16; s *= 2)
@@ -637,10 +658,11 @@ cudaError_t launch_vec(ScanArgs a, cudaStream_t st) {
     a.blocks_per_group = (a.dpg + C::CH - 1) / C::CH;
     const long long blocks = (long long)a.B * a.G * a.blocks_per_group;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    const int segments = segments_of(blocks * C::WARPS, a.L, C::TT);
+    const size_t cut_smem = sizeof(typename C::Smem) + sizeof(typename C::Segment);
+    const int segments = segments_of(blocks, cut_smem, SPT, a.L, C::TT);
     auto kern = segments > 1 ? selective_scan_kernel<T, SPT, LANES, VEC, true>
                              : selective_scan_kernel<T, SPT, LANES, VEC, false>;
-    const size_t smem = sizeof(typename C::Smem) + (segments > 1 ? sizeof(typename C::Segment) : 0);
+    const size_t smem = segments > 1 ? cut_smem : sizeof(typename C::Smem);
     cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (err != cudaSuccess) return err;
     if (segments > 8) {
