@@ -473,12 +473,21 @@ selective_scan_kernel(const ScanArgs a) {
 // (a power of two, two where N allows, so that a read covers whole 32-byte
 // sectors) share the channel, and u, d and the step's softplus are worked out once
 // per thread.  Several sequences per thread (A read once for them) measured
-// slower, since the registers cost resident warps: 64 x 4096 x 16 states 13.0 us
-// with four, 10.6 with one.  ONE: L = 1 (9.2 -> 8.6 us for the same).  The tiles of
-// 16 rows above took 36 us for one token there, and half of each tile is idle up to
-// kTokenRows.
-constexpr int kTokenRows = 8;  // longest L
+// slower, since the registers cost resident warps.  ONE: L = 1, 10.2 us for one bf16
+// token of 64 x 4096 x 16 states (floor 5.6), f32 8.9.
 constexpr int kTokenThreads = 128;
+// Longest L: the rows go one after the other here, while a tile above takes 16 rows in
+// the time of one, but has a CTA's start and the reads of whole tiles before it.
+// Measured, us here / tiles, for 5 and 8 rows, 16 states if not said:
+//    1 x  512 channels, bf16   5.1 / 4.4    7.0 / 4.5
+//    8 x 1024           bf16   5.4 / 4.5    7.2 / 4.5      fp32   4.9 / 4.5    6.6 / 4.6
+//      64 states        bf16   7.0 / 6.8    9.4 / 6.8      fp32   5.8 / 7.2    7.8 / 7.2
+//    8 x 4096           bf16   6.3 / 7.5    8.8 / 7.5      fp32   5.6 / 9.1    7.6 / 9.2
+//   16 x 4096           bf16   8.9 / 11.8  12.8 / 11.8     fp32   8.2 / 13.4  11.1 / 13.6
+//      128 states       bf16  53.2 / 76.0  79.8 / 75.9     fp32  44.6 / 100   68.4 / 101
+//   64 x 4096           bf16  30 / 40      46.6 / 41.2     fp32  29 / 48      45.5 / 49.3
+// (9 rows: 9.5 / 7.7, 14.1 / 11.8, 53.0 / 41.4 bf16, 50.3 / 50.4 fp32 of the last).
+inline int token_rows(long long threads) { return threads < 48 * 1024 ? 5 : 8; }
 
 template <typename T, int V, bool VEC, bool ONE>
 __global__ void __launch_bounds__(kTokenThreads)
@@ -606,14 +615,15 @@ cudaError_t launch_token_t(const ScanArgs &a, int lanes, cudaStream_t st) {
     return err;
 }
 
+// Threads that share a channel's states in the kernel of few rows.
+inline int token_lanes(int N) { return N <= 4 ? 1 : N <= 16 ? 2 : N <= 64 ? 4 : 8; }
+
 template <typename T>
 cudaError_t launch_tokens(const ScanArgs &a, cudaStream_t st) {
-    if (a.N <= 4) return launch_token_t<T, 1>(a, 1, st);
-    if (a.N <= 8) return launch_token_t<T, 1>(a, 2, st);
-    if (a.N <= 16) return launch_token_t<T, 2>(a, 2, st);
-    if (a.N <= 32) return launch_token_t<T, 2>(a, 4, st);
-    if (a.N <= 64) return launch_token_t<T, 4>(a, 4, st);
-    return launch_token_t<T, 4>(a, 8, st);
+    const int lanes = token_lanes(a.N);
+    if (a.N <= 8) return launch_token_t<T, 1>(a, lanes, st);
+    if (a.N <= 32) return launch_token_t<T, 2>(a, lanes, st);
+    return launch_token_t<T, 4>(a, lanes, st);
 }
 
 // Segments that a sequence of L rows is cut into, 1, 4, 8 or 16, by the time that
@@ -698,7 +708,8 @@ cudaError_t launch_scan(const ScanArgs &a, cudaStream_t st) {
 
 template <typename T>
 cudaError_t launch_n(const ScanArgs &a, cudaStream_t st) {
-    if (a.L <= kTokenRows && a.B <= 65535) return launch_tokens<T>(a, st);
+    const long long threads = (long long)a.B * a.D * token_lanes(a.N);
+    if (a.L <= token_rows(threads) && a.B <= 65535) return launch_tokens<T>(a, st);
     if (a.N <= 8) return launch_scan<T, 4, 2>(a, st);
     if (a.N <= 16) return launch_scan<T, 8, 2>(a, st);
     if (a.N <= 32) return launch_scan<T, 8, 4>(a, st);

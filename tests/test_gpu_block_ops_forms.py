@@ -163,6 +163,16 @@ def test_scan_within_its_counted_roundings(D, N, G, pad, off, dtype, L):
     scan_and_check(c, dtype, [L, 0, (L + 1) // 2], gate=False, pad=pad, off=off)
 
 
+@pytest.mark.parametrize("L", [6, 8])
+@pytest.mark.parametrize("B,D,N,G", [(8, 4096, 16, 1), (12, 4100, 5, 2), (13, 1030, 64, 1), (7, 1032, 128, 4)])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_scan_of_a_few_rows_and_many_channels(B, D, N, G, dtype, L):
+    """(as many as the kernel of few rows takes 6 to 8 of)"""
+    c = scan_case(B, L, D, N, G, dtype, seed=63)
+    scan_and_check(c, dtype, None, gate=False)
+    scan_and_check(c, dtype, [L, 0, 1, L - 1, 5, 2, 3] + [L] * (B - 7), in_place=False, pad=1)
+
+
 # ------------------------------------------------------------------------ together
 @pytest.mark.parametrize("T", [1, 3])
 def test_norm_and_4_bit_products_around_the_recurrent_step(T):
