@@ -357,21 +357,28 @@ cudaError_t launch_w4(W4Args a, cudaStream_t st) {
     const int per = a.x_dtype == RET_F32 ? 3 : 1;
     a.tile_cols = std::min(a.cols, NT * 8 / per * per);  // whole rows of x
     const int groups = a.K / (32 * WPL);
-    const long long tiles = ((long long)a.N + 15) / 16;
+    const long long tiles = ((long long)a.N + 15) / 16, by = (a.cols + a.tile_cols - 1) / a.tile_cols;
     const size_t x_bytes = (size_t)a.K * 2 * a.tile_cols;
     auto unit = [&](int wk) { return 32 * WPL * PF * wk; };  // columns: one ring of each warp
     // The CTA that leaves the fullest SM least to do, counted in instructions (a
-    // group's, x's staging and a CTA's own), each tile of rows shared by as many
-    // warps as fit, down to two groups each.  (One token times 2048 x 12288, before
-    // the unpacking got faster: 6.9 us with 6 tiles of 2 warps (128 CTAs), 8.2 with 2
-    // of 4, 10.5 with 1 of 8.)
+    // group's, x's staging and a CTA's own; read off the code, not fitted), each tile
+    // of rows shared by as many warps as fit, down to two groups each.  us by tiles of
+    // a CTA, * chosen: one bf16 row times 2048 x 12288 9.4 (1), 10.0 (2), 6.6* (6), 9.7
+    // (12); times 8192 x 28672 63 (1), 50 (2), 41 (7), 38* (14); 16 int8 rows 180 (1),
+    // 120 (2), 71 (7), 58* (13); 64 bf16 rows times 4096 x 14336 378 (1), 144 (2), 76*
+    // (7), 70 (8); 64 fp32 rows times 4096 x 4096 201 (1), 95 (2), 60* (7), 61 (8); 48
+    // bf16 rows times 2048 x 2048 in groups of 32 26* (1), 22 (2), 48 (8).  Over 16
+    // shapes of 1 to 64 rows it is within 10% of the best but for small weights and
+    // many rows (16 and 18%).
     const int most = max_threads(NT) / 32;
     double best = 1e300;
     for (int wr = most; wr >= 1; --wr) {
         int wk = std::max(1, std::min(most / wr, groups / 2));
         while (wk > 1 && x_bytes > kStage && (size_t)unit(wk) * 2 * a.tile_cols > 2 * kStage) --wk;
-        const double ctas = (double)(((tiles + wr - 1) / wr + kSms - 1) / kSms);
-        const double group = (wr * wk) * (double)((groups + wk - 1) / wk) * (WPL * (30 + 4 * NT) + 60 + 8 * NT);
+        const double ctas = (double)(((tiles + wr - 1) / wr * by + kSms - 1) / kSms);
+        // (a CTA of fewer warps than fit takes as long as a nearly full one)
+        const double warps = std::max(wr * wk, most * 7 / 8) + 0.01 * wr * wk;
+        const double group = warps * (double)((groups + wk - 1) / wk) * (WPL * (30 + 4 * NT) + 60 + 8 * NT);
         const double cost = ctas * (group + (double)a.K * a.tile_cols / 256 * 20 + 3000);
         if (cost < best) {
             best = cost;
@@ -383,7 +390,7 @@ cudaError_t launch_w4(W4Args a, cudaStream_t st) {
     a.kc = x_bytes <= kStage ? a.K : std::max(1, (int)(kStage / (2 * a.tile_cols) / unit(a.wk))) * unit(a.wk);
     if (a.kc > a.K) a.kc = a.K;
     const size_t smem = std::max((size_t)a.kc * 2 * a.tile_cols, sizeof(float) * a.wk * a.wr * 16 * (NT * 8 + 1));
-    const long long bx = (tiles + a.wr - 1) / a.wr, by = (a.cols + a.tile_cols - 1) / a.tile_cols;
+    const long long bx = (tiles + a.wr - 1) / a.wr;
     auto kern = a.zeros ? a.xgrouped ? matvec_w4_kernel<WPL, NT, PF, true, true> : matvec_w4_kernel<WPL, NT, PF, true, false>
                         : a.xgrouped ? matvec_w4_kernel<WPL, NT, PF, false, true> : matvec_w4_kernel<WPL, NT, PF, false, false>;
     // (the same limit in every call: calls of other sizes may run at once)
