@@ -553,7 +553,9 @@ ret_status ret_gate_norm_backward(int B, int L, int H, int d_v, int o_dtype,
  * with top = 127 for RET_I8 and 448 for RET_E4M3, to nearest even.  A group
  * whose scale would be below 2^-119 (all zeros, say) has scale 0 and codes 0;
  * one with a y that is not finite has scale NaN (codes 0), so that every value
- * it stands for is NaN.
+ * it stands for is NaN.  The sum of s^2 and the products w s are fp32 numbers:
+ * rows with |s| from about 10^19 on come out as zeros, and with eps = 0 those
+ * below 10^-19 as infinities or with few bits.
  *   X       device x_dtype (F32, BF16), strided rows of d
  *   w       device fp32 [d], or NULL (ones)
  *   R       device r_dtype (F32, BF16) [rows][d], or NULL (no residual)
@@ -612,7 +614,9 @@ typedef struct {
  *     y_t = (sum_n C_t[g][n] h_t[n] + skip u_t) swish(z_t)
  * (update first, then read, as ret_recurrent_step).  The sibling of
  * ret_chunkwise with a decay per token, channel and state.  A is meant to be
- * negative.
+ * negative; states may grow where they stay fp32 numbers, and a row's
+ * exp(d_t A) too.  From a row on whose d_t u_t is not finite, the channel's
+ * outputs and states are not (infinite or NaN, not always as in the formula).
  *   U, delta, Z  device dtype, strided rows of D (row t of sequence b is row
  *           b*L + t); Z NULL: no gate
  *   Bm, Cm  device dtype, strided rows of G*N

@@ -6,11 +6,15 @@
 // Bound by HBM: x and r are read once, r_out and y written once.  A row is
 // spread over `tpr` threads (a power of two, one warp or more) that hold it in
 // registers between the sum of squares and the output, kVec adjacent channels per
-// thread and step, all requested before any is used, so nothing is read twice; the
-// arithmetic runs on pairs.  The largest |w s| of a row comes out of the same
+// thread and step, so nothing is read twice; all of x and r is requested before any is
+// used, the weights (from L2) step by step.  The arithmetic runs on pairs.  The largest |w s| of a row comes out of the same
 // reduction as the sum of squares (|y| = |w s| / rms), so the 8-bit scale of a
 // whole row needs no second one, and that of a group of 32, 64 or 128 channels
 // only shuffles among 4, 8 or 16 lanes.
+//
+// With a residual, us (share of the measured copy bandwidth): 32768 bf16 rows of 2048
+// to bf16 80 (103%), to e4m3 with groups of 128 94 (78%); 8192 rows of 16384 in bf16
+// 202 (82%), in fp32 432 (77%; there 116 bytes a thread are spilled).
 #include <cuda_fp8.h>
 
 #include <cmath>

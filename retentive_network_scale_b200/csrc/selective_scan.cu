@@ -140,12 +140,14 @@ struct ScanTile {
 // units (16 a clock and SM), 478 us for 8 x 4096 rows of 4096 channels with 16
 // states, next to some 60 instructions a row for a warp's 16 channels and the reads
 // of B and C, which return 128 bytes a clock however many lanes read the same.
-// Measured 869 us there, 165 us being the floor of its bytes.  Measured and not
+// Measured 867 us there, 165 us being the floor of its bytes.  Measured and not
 // kept: 4 threads a channel (942 us; 1085 with one register pair of du in place of
 // two copies), 2 channels a thread (945), a polynomial for a quarter of the
 // exponentials (991), unpacked arithmetic (992): what costs is instructions and
 // shared memory as much as the exponentials, and 2048 warps are 3.5 a scheduler,
-// of which the fullest have 4.
+// of which the fullest have 4.  More states, 8 x 2048 rows of 2048 channels, us (their
+// exponentials alone): 24 453 (179; computed as 32), 32 450 (239), 64 770 (477), 128
+// 1413 (954).
 //
 // SPLIT (few channels): a cluster of CTAs shares the channels, each CTA one segment
 // of the rows.  1 x 16384 rows of 1024 channels: 1462 us in one piece, 443 in 8
