@@ -554,8 +554,8 @@ ret_status ret_gate_norm_backward(int B, int L, int H, int d_v, int o_dtype,
  * whose scale would be below 2^-119 (all zeros, say) has scale 0 and codes 0;
  * one with a y that is not finite has scale NaN (codes 0), so that every value
  * it stands for is NaN.  The sum of s^2 and the products w s are fp32 numbers:
- * rows with |s| from about 10^19 on come out as zeros, and with eps = 0 those
- * below 10^-19 as infinities or with few bits.
+ * a row whose sum passes 3.4e38 comes out as zeros, and with eps = 0 one below
+ * some 10^-19 as infinities or with few bits.
  *   X       device x_dtype (F32, BF16), strided rows of d
  *   w       device fp32 [d], or NULL (ones)
  *   R       device r_dtype (F32, BF16) [rows][d], or NULL (no residual)
