@@ -218,6 +218,15 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _result(shape, dtype, device, stream):
+    """_empty for what a call returns: the caller may let go of it with work on the
+    current stream still to read it, which the block then waits for."""
+    t = _empty(shape, dtype, device, stream)
+    if stream is not None:
+        t.record_stream(torch.cuda.current_stream(t.device))
+    return t
+
+
 def make_desc(B, H, L, d_k, d_v, in_dtype, out_dtype, gamma, rotate=False,
               theta_base=10000.0, pos_offset=0):
     if len(gamma) != H:
@@ -387,7 +396,7 @@ def ret_msr_layer(X, W_qkvg, W_o, gamma, chunk, d_k, d_v, out=None, gn_eps=1e-5,
     _dev(X, "X", dtype=torch.bfloat16); _dev(W_qkvg, "W_qkvg", (dm, n_proj), torch.bfloat16)
     _dev(W_o, "W_o", (H * d_v, dm), torch.bfloat16)
     if out is None:
-        out = _empty((B, L, dm), torch.bfloat16, X.device, stream)
+        out = _result((B, L, dm), torch.bfloat16, X.device, stream)
     _dev(out, "out", (B, L, dm), torch.bfloat16)
     d = make_desc(B, H, L, d_k, d_v, RET_BF16, RET_BF16, gamma, rotate, theta_base, pos_offset)
     need = int(lib.ret_msr_layer_workspace_size(ctypes.byref(d), int(dm), int(chunk)))
@@ -414,7 +423,7 @@ def ret_gemm_bf16(A, B, C=None, stream=None):
     if K2 != K:
         raise ValueError("inner sizes differ")
     if C is None:
-        C = _empty((M, N), torch.bfloat16, A.device, stream)
+        C = _result((M, N), torch.bfloat16, A.device, stream)
     if not C.is_cuda or C.dim() != 2 or C.stride(1) != 1 or tuple(C.shape) != (M, N) \
             or C.dtype != torch.bfloat16:
         raise ValueError("C must be a 2-D bf16 CUDA tensor [M, N] with unit row stride")
@@ -440,7 +449,7 @@ def ret_backward(Q, K, V, dO, gamma, chunk, dQ=None, dK=None, dV=None, out_dtype
     dv = V.shape[-1]
     _dev(Q, "Q", dtype=torch.bfloat16); _dev(K, "K", Q.shape, torch.bfloat16)
     _dev(V, "V", (B, H, L, dv), torch.bfloat16); _dev(dO, "dO", (B, H, L, dv), torch.bfloat16)
-    mk = lambda t, shape: t if t is not None else _empty(shape, out_dtype, Q.device, stream)  # noqa: E731
+    mk = lambda t, shape: t if t is not None else _result(shape, out_dtype, Q.device, stream)  # noqa: E731
     dQ, dK, dV = mk(dQ, (B, H, L, dk)), mk(dK, (B, H, L, dk)), mk(dV, (B, H, L, dv))
     _dev(dQ, "dQ", (B, H, L, dk)); _dev(dK, "dK", (B, H, L, dk), dQ.dtype)
     _dev(dV, "dV", (B, H, L, dv), dQ.dtype)
@@ -472,7 +481,7 @@ def ret_segment_state(K, V, gamma, U=None, rotate=False, theta_base=10000.0, pos
     dv = V.shape[-1]
     _dev(K, "K", dtype=torch.bfloat16); _dev(V, "V", (B, H, L, dv), torch.bfloat16)
     if U is None:
-        U = _empty((B, H, dk, dv), torch.float32, K.device, stream)
+        U = _result((B, H, dk, dv), torch.float32, K.device, stream)
     _dev(U, "U", (B, H, dk, dv), torch.float32)
     d = make_desc(B, H, L, dk, dv, RET_BF16, RET_F32, gamma, rotate, theta_base, pos_offset)
     need = int(lib.ret_segment_state_workspace_size(ctypes.byref(d)))
@@ -501,7 +510,7 @@ def ret_state_scan(U_all, seg_lens, rank, gamma, state_in=None, R=None, stream=N
     if state_in is not None:
         _dev(state_in, "state_in", (B, H, dk, dv), torch.float32)
     if R is None:
-        R = _empty((B, H, dk, dv), torch.float32, U_all.device, stream)
+        R = _result((B, H, dk, dv), torch.float32, U_all.device, stream)
     _dev(R, "R", (B, H, dk, dv), torch.float32)
     lens = (ctypes.c_int * len(seg_lens))(*[int(x) for x in seg_lens])
     d = make_desc(B, H, 0, dk, dv, RET_F32, RET_F32, gamma)
@@ -523,7 +532,7 @@ def ret_chunkwise_segmented(Q, K, V, gamma, chunk, segments, O=None, state_in=No
     _dev(Q, "Q", dtype=torch.bfloat16); _dev(K, "K", Q.shape, torch.bfloat16)
     _dev(V, "V", (B, H, L, dv), torch.bfloat16)
     if O is None:
-        O = _empty((B, H, L, dv), out_dtype, Q.device, stream)
+        O = _result((B, H, L, dv), out_dtype, Q.device, stream)
     _dev(O, "O", (B, H, L, dv))
     _dev(state_in, "state_in", (B, H, dk, dv), torch.float32)
     _dev(state_out, "state_out", (B, H, dk, dv), torch.float32)
@@ -940,10 +949,10 @@ def ret_quantize_w4(W, group, zeros=False, stream=None):
     if K > _INT_MAX or N > _INT_MAX or group > _INT_MAX:
         _refuse_sizes(K, N, group)
     pw, ldw = _rows(W, "W", W.shape, W.dtype, device)
-    wq = _empty((N, K // 2), torch.uint8, W.device, stream)
+    wq = _result((N, K // 2), torch.uint8, W.device, stream)
     groups = K // group if group > 0 else 0
-    scales = _empty((N, groups), torch.bfloat16, W.device, stream)
-    zp = _empty((N, groups), torch.uint8, W.device, stream) if zeros else None
+    scales = _result((N, groups), torch.bfloat16, W.device, stream)
+    zp = _result((N, groups), torch.uint8, W.device, stream) if zeros else None
     _check(load_library().ret_quantize_w4(K, N, int(group), _dtype_code(W), pw, ldw, wq.data_ptr(),
                                           scales.data_ptr(), None if zp is None else zp.data_ptr(),
                                           _on_stream(stream, device)), "ret_quantize_w4")

@@ -22,11 +22,16 @@ class FakeLibrary:
         return call
 
 
+class Made(list):
+    recorded = 0
+
+
 @pytest.fixture
 def streams(monkeypatch):
     """Stands in for torch's streams; returns the (stream, bytes) of each allocation
-    (the stream being None for the current one)."""
-    inside, made, empty = [None], [], torch.empty
+    (the stream being None for the current one).  Blocks that wait for the current
+    stream's work when they are let go of are counted in `recorded`."""
+    inside, made, empty = [None], Made(), torch.empty
 
     class Stream:
         def __init__(self, handle=0, device=None):
@@ -44,6 +49,12 @@ def streams(monkeypatch):
         made.append((inside[-1], t.numel() * t.element_size()))
         return t
 
+    def record(t, stream):
+        assert stream == "current"
+        made.recorded += 1
+
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: "current")
+    monkeypatch.setattr(torch.Tensor, "record_stream", record)
     monkeypatch.setattr(torch.cuda, "Stream", Stream)
     monkeypatch.setattr(torch.cuda, "ExternalStream", Stream)
     monkeypatch.setattr(torch.cuda, "stream", use)
@@ -59,7 +70,7 @@ def test_quantize_w4_makes_its_results_on_its_stream(streams):
     W = torch.zeros(128, 8)
     side = torch.cuda.Stream(0x40)
     R.ret_quantize_w4(W, 64, zeros=True, stream=side)
-    assert [s for s, _ in streams] == [side] * 3
+    assert [s for s, _ in streams] == [side] * 3 and streams.recorded == 3
     streams.clear()
     R.ret_quantize_w4(W, 64, zeros=True, stream=0x80)           # a raw handle
     assert [s.cuda_stream for s, _ in streams] == [0x80] * 3
@@ -77,23 +88,26 @@ def test_workspaces_and_results_of_every_call_are_made_on_its_stream(streams, mo
     b, bv, G = q.bfloat16(), v.bfloat16(), torch.zeros(B, L, H * dv)
     x, w = torch.zeros(B, L, 8).bfloat16(), torch.zeros(8, H * (2 * dk + 2 * dv)).bfloat16()
     w_o, U = torch.zeros(H * dv, 8).bfloat16(), torch.zeros(2, B, H, dk, dv)
+    # allocations of a call, and how many of them it returns
     calls = [
-        (1, lambda s: R.ret_parallel(q, q, v, v, gamma, stream=s)),
-        (1, lambda s: R.ret_chunkwise(q, q, v, gamma, chunk, O=v, stream=s)),
-        (1, lambda s: R.ret_chunkwise_host(q, q, v, gamma, chunk, O=v, stream=s)),
-        (2, lambda s: R.ret_msr_layer(x, w, w_o, gamma, chunk, dk, dv, stream=s)),
-        (4, lambda s: R.ret_backward(b, b, bv, bv, gamma, chunk, stream=s)),
-        (2, lambda s: R.ret_segment_state(b, bv, gamma, stream=s)),
-        (1, lambda s: R.ret_state_scan(U, [4, 4], 1, gamma, stream=s)),
-        (2, lambda s: R.ret_chunkwise_segmented(b, b, bv, gamma, chunk, 2, stream=s)),
+        (1, 0, lambda s: R.ret_parallel(q, q, v, v, gamma, stream=s)),
+        (1, 0, lambda s: R.ret_chunkwise(q, q, v, gamma, chunk, O=v, stream=s)),
+        (1, 0, lambda s: R.ret_chunkwise_host(q, q, v, gamma, chunk, O=v, stream=s)),
+        (2, 1, lambda s: R.ret_msr_layer(x, w, w_o, gamma, chunk, dk, dv, stream=s)),
+        (4, 3, lambda s: R.ret_backward(b, b, bv, bv, gamma, chunk, stream=s)),
+        (2, 1, lambda s: R.ret_segment_state(b, bv, gamma, stream=s)),
+        (1, 1, lambda s: R.ret_state_scan(U, [4, 4], 1, gamma, stream=s)),
+        (2, 1, lambda s: R.ret_chunkwise_segmented(b, b, bv, gamma, chunk, 2, stream=s)),
     ]
     monkeypatch.setattr(R, "_stream", lambda s: R.ctypes.c_void_p(0))
     side = torch.cuda.Stream(0x40)
-    for n, call in calls:
+    for n, returned, call in calls:
         for stream in (side, None):
             streams.clear()
+            streams.recorded = 0
             call(stream)
             assert [s for s, _ in streams] == [stream] * n
+            assert streams.recorded == (returned if stream else 0)
 
 
 def test_binding_imports_on_a_torch_without_cuda(monkeypatch):

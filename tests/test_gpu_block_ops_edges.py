@@ -326,3 +326,47 @@ def test_calls_with_workspaces_on_another_stream(raw):
         torch.cuda.synchronize()
         assert all(torch.equal(x, y) for x, y in zip(want, whole(got)))
         del blocks
+
+
+def test_result_of_another_stream_let_go_of_early():
+    """The caller's stream reads a result that was made on another one, and the
+    next call there may not have its memory before that."""
+    W, W2 = rt((1024, 2048), 18).cuda(), rt((1024, 2048), 19).cuda()
+    want = R.ret_quantize_w4(W, 64)[0].clone()
+    a, b = rt((512, 256), 20, 1.0, BF16).cuda(), rt((256, 512), 21, 1.0, BF16).cuda()
+    product = R.ret_gemm_bf16(a, b).clone()
+    side, zero = torch.cuda.Stream(), torch.zeros_like(a)
+    torch.cuda.synchronize()
+    for raw in (False, True):
+        stream = side.cuda_stream if raw else side
+        codes, c = R.ret_quantize_w4(W, 64, stream=stream)[0], R.ret_gemm_bf16(a, b, stream=stream)
+        torch.cuda.current_stream().wait_stream(side)
+        torch.cuda._sleep(int(5e7))
+        got, c2 = codes.clone(), c.clone()
+        del codes, c
+        R.ret_quantize_w4(W2, 64, stream=stream)
+        R.ret_gemm_bf16(zero, b, stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want) and torch.equal(c2, product)
+
+
+def test_calls_that_allocate_captured_on_two_streams():
+    """A graph of calls on the capturing stream and on one that joins it."""
+    W = rt((512, 256), 22).cuda()
+    b = rt((256, 512), 23, 1.0, BF16).cuda()
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    want = R.ret_quantize_w4(W, 64, zeros=True), R.ret_gemm_bf16(W.to(BF16), b)
+    x, y = torch.zeros_like(W), torch.zeros_like(W.to(BF16))
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        here = torch.cuda.current_stream()
+        side.wait_stream(here)
+        q = R.ret_quantize_w4(x, 64, zeros=True, stream=side)
+        R.ret_quantize_w4(x, 32, stream=side)                   # let go of at once
+        c = R.ret_gemm_bf16(y, b, stream=here)
+        here.wait_stream(side)
+    x.copy_(W)
+    y.copy_(W)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(s, t) for s, t in zip(q, want[0])) and torch.equal(c, want[1])
