@@ -488,7 +488,7 @@ constexpr int kTokenThreads = 128;
 //   16 x 4096           bf16   8.9 / 11.8  12.8 / 11.8     fp32   8.2 / 13.4  11.1 / 13.6
 //      128 states       bf16  53.2 / 76.0  79.8 / 75.9     fp32  44.6 / 100   68.4 / 101
 //   64 x 4096           bf16  30 / 40      46.6 / 41.2     fp32  29 / 48      45.5 / 49.3
-// (9 rows: 9.5 / 7.7, 14.1 / 11.8, 53.0 / 41.4 bf16, 50.3 / 50.4 fp32 of the last).
+// 9 rows, bf16: 9.5 / 7.7 (8 x 4096), 14.1 / 11.8 (16 x 4096), 53.0 / 41.4 (64 x 4096).
 inline int token_rows(long long threads) { return threads < 48 * 1024 ? 5 : 8; }
 
 template <typename T, int V, bool VEC, bool ONE>
@@ -603,7 +603,6 @@ selective_token_kernel(const ScanArgs a, int lanes) {
 template <typename T, int V>
 cudaError_t launch_token_t(const ScanArgs &a, int lanes, cudaStream_t st) {
     const long long bx = ((long long)a.D * lanes + kTokenThreads - 1) / kTokenThreads;
-    if ((long long)a.D * lanes > 0x7fffff00LL || a.B > 65535) return cudaErrorInvalidConfiguration;
     // whole float4s of states, and 4-element pieces of B and C on their size
     auto fits = [](const void *p, long long ld) {
         return (reinterpret_cast<uintptr_t>(p) & (4 * sizeof(T) - 1)) == 0 && ld % 4 == 0;
@@ -710,8 +709,9 @@ cudaError_t launch_scan(const ScanArgs &a, cudaStream_t st) {
 
 template <typename T>
 cudaError_t launch_n(const ScanArgs &a, cudaStream_t st) {
-    const long long threads = (long long)a.B * a.D * token_lanes(a.N);
-    if (a.L <= token_rows(threads) && a.B <= 65535) return launch_tokens<T>(a, st);
+    // (its grid: threads of a sequence in an int, sequences in y)
+    const long long threads = (long long)a.D * token_lanes(a.N);
+    if (a.L <= token_rows(a.B * threads) && threads <= 0x7fffff00LL && a.B <= 65535) return launch_tokens<T>(a, st);
     if (a.N <= 8) return launch_scan<T, 4, 2>(a, st);
     if (a.N <= 16) return launch_scan<T, 8, 2>(a, st);
     if (a.N <= 32) return launch_scan<T, 8, 4>(a, st);

@@ -174,6 +174,21 @@ def test_conv_of_the_most_channels_a_call_takes():
     assert torch.equal(y[0, 0, -256:], 2 * x[0, 0, -256:]) and bool((y[0, 0, :4096] == 0).all())
 
 
+def test_scan_token_of_more_channels_than_its_threads_count():
+    """Two threads a channel, whose number passes 2^31: taken by the tiles."""
+    D, N, n = 2 ** 30 + 40, 5, 200
+    c = {k: rt((1, 1, n), 34 + i, 1.0, BF16) for i, k in enumerate("ud")}
+    A, bm = -rt((n, N), 36).abs(), rt((1, 1, 1, N), 37, 1.0, BF16)
+    u, d = (torch.zeros(1, 1, D, device="cuda", dtype=BF16) for _ in range(2))
+    wide = torch.zeros(D, N, device="cuda")
+    u[..., -n:], d[..., -n:], wide[-n:] = c["u"].cuda(), c["d"].cuda(), A.cuda()
+    y = torch.full_like(u, 5.0)
+    R.ret_selective_scan(u, d, wide, bm.cuda(), bm.cuda(), y)
+    want, _, tol, _ = ref.selective_scan(c["u"], c["d"], A, bm, bm)
+    assert ref.within(y[..., -n:], want, tol + ref.rounded(want, BF16)) <= 1
+    assert bool((y[..., :-n] == 0).all())
+
+
 # ------------------------------------------------------------------------ 4-bit product
 @pytest.mark.parametrize("g", [32, 64, 128])
 @pytest.mark.parametrize("M", [1, 2, 5, 10, 22, 64])
